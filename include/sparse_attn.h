@@ -59,7 +59,9 @@ typedef enum {
     SA_ERR_DEVICE_TIMEOUT = 6  /* a kernel's bounded wait ran out (see check_device) */
 } sa_status;
 
-typedef enum { SA_BF16 = 0, SA_FP32 = 1 } sa_dtype;
+/* SA_E4M3 (8-bit floats, 4 exponent and 3 mantissa bits, largest value 448)
+ * is a storage type of the paged cache only. */
+typedef enum { SA_BF16 = 0, SA_FP32 = 1, SA_E4M3 = 2 } sa_dtype;
 
 /* A contiguous [B, H, T, D] tensor in device memory.  `dtype` is an sa_dtype. */
 typedef struct {
@@ -189,6 +191,124 @@ sa_status sparse_attn_bwd_noalloc(const sa_tensor *q, const sa_tensor *k, const 
 sa_status sparse_attn_decode(const sa_tensor *q, const sa_tensor *k_cache,
                              const sa_tensor *v_cache, const int64_t *pos, sa_graph g,
                              float scale, sa_tensor *out, float *lse, void *stream);
+
+/* ------------------------------------------------------------ paged cache */
+
+/* A key-value cache in pages of page_size rows, shared by all requests of a
+ * server: row s of a request's page lies at [page, h, s, :] of k and v, each
+ * contiguous [n_pages, Hkv, page_size, D], D in {32, 64, 128}, 16-byte
+ * aligned.  dtype SA_BF16, SA_FP32 or SA_E4M3; for SA_E4M3 every row of k
+ * and v has its own fp32 scale in k_scale, v_scale [n_pages, Hkv, page_size]
+ * (a row's values are code * scale), else both are NULL.
+ *
+ * A block table is DEVICE int32 [rows, max_pages]: entry [b, p] is the page
+ * that holds the positions p * page_size ... of request b.  A page may stand
+ * in several rows (a shared prompt).  max_pages * page_size, n_pages and
+ * rows < 2^31.  A slot is page * page_size + row, the address of one cached
+ * position. */
+typedef struct {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int32_t dtype;
+    int64_t n_pages, Hkv, page_size, D;
+} sa_paged_cache;
+
+/* What becomes of a request in a step (sa_paged_step.status). */
+typedef enum {
+    SA_PAGED_OK = 0,
+    SA_PAGED_NO_PAGES = 1, /* not enough free pages: nothing done for it */
+    SA_PAGED_REFUSED = 2   /* len or n_new out of range, longer than its
+                              block-table row, past `capacity`, or its pages
+                              do not fit on the stack: nothing done for it */
+} sa_paged_status;
+
+/* The bookkeeping of one step of a server, all arrays in DEVICE memory.
+ * Request b has len[b] cached positions in the pages of its block-table row
+ * and brings n_new[b] >= 0 new tokens, or has finished (n_new[b] = -1).  Free
+ * pages lie on a stack: free_pages[0 .. *free_count).
+ *   1. The pages of finished requests go on top of the stack, in the order
+ *      (request, page); their length becomes 0.  Uses are not counted: a
+ *      page that stands in two rows (a shared prompt) would go on the stack
+ *      with each of them, so of those rows only the last in use may be
+ *      finished here; the owner clears the others' lengths.
+ *   2. The others take the pages that their new tokens need from the top, in
+ *      the order of the requests, the page on top first.  If those left do
+ *      not cover a request's need, it and every later request that needs a
+ *      page get SA_PAGED_NO_PAGES (first come, first served: none overtakes).
+ *   3. cu_new[0 .. B] is the exclusive prefix sum of max(n_new, 0), refused
+ *      requests included: request b owns tokens cu_new[b] .. cu_new[b+1).
+ *      Token t of an accepted request gets row[t] = b, its position pos[t]
+ *      and its slot[t] (-1 if its page's entry is negative); the tokens of
+ *      refused requests and the entries from cu_new[B] to capacity get -1 in
+ *      all three.
+ * len_out and free_count_out receive the new lengths and count; they may be
+ * len and free_count themselves (the step then advances in place, also when a
+ * captured graph is replayed).  No other arrays may overlap.  Entries of
+ * block_table other than newly taken pages, and of free_pages other than
+ * returned ones, stay as they were.  A free_count outside [0, n_stack] means
+ * that no page is taken or returned.  1 <= B <= SA_PAGED_MAX_REQUESTS;
+ * capacity and n_stack >= 1 and < 2^31. */
+#define SA_PAGED_MAX_REQUESTS 8192
+typedef struct {
+    int64_t B, max_pages, page_size, capacity, n_stack;
+    const int64_t *len;        /* [B] */
+    const int32_t *n_new;      /* [B] */
+    int32_t *block_table;      /* [B, max_pages] */
+    int32_t *free_pages;       /* [n_stack] */
+    const int64_t *free_count; /* [1] */
+    int64_t *len_out;          /* [B] */
+    int64_t *free_count_out;   /* [1] */
+    int64_t *cu_new;           /* [B + 1] */
+    int64_t *slot, *pos;       /* [capacity] */
+    int32_t *row;              /* [capacity] */
+    int32_t *status;           /* [B] */
+} sa_paged_step;
+
+/* Plan a step: one launch, no workspace, no host synchronisation. */
+sa_status sparse_attn_paged_plan(const sa_paged_step *step, void *stream);
+
+/* Write new key and value rows into the cache.  k_new, v_new: [N, Hkv, 1, D]
+ * with k_stride, v_stride elements from token to token (at least Hkv * D, a
+ * multiple of 16 bytes; the heads of one token are contiguous), so that both
+ * may be slices of a fused projection.  slot: DEVICE int64 [N].  Row t goes
+ * to slot[t]; a negative slot is skipped, one outside the cache too, and that
+ * flags the device error word.  The slots of one call are distinct (of a slot
+ * named twice some mixture of its rows is stored).  The new rows have the
+ * cache's dtype, or SA_BF16 for an SA_E4M3 cache, where row x is stored as
+ *     scale = max_d |x_d| / 448,   code_d = e4m3(x_d / scale)
+ * (round to nearest even; all codes 0 when scale is 0; scale NaN and codes 0
+ * when the row holds an infinity or a NaN).  No workspace. */
+sa_status sparse_attn_paged_append(const sa_tensor *k_new, int64_t k_stride,
+                                   const sa_tensor *v_new, int64_t v_stride, const int64_t *slot,
+                                   const sa_paged_cache *cache, void *stream);
+
+/* Bytes of workspace sparse_attn_paged_decode needs for these shapes (it
+ * depends on q's head count, the cache and the graph, not on positions); 0 if
+ * it needs none. */
+size_t sparse_attn_paged_decode_workspace_size(const sa_tensor *q, const sa_paged_cache *cache,
+                                               sa_graph g);
+
+/* sparse_attn_decode against a paged cache: one query per new token.  q, out:
+ * [N, H, 1, D], H a multiple of the cache's Hkv, dtype that of the cache
+ * (SA_BF16 for SA_E4M3).  Token t stands at position pos[t] (DEVICE int64
+ * [N]) of the request in block-table row row[t] (DEVICE int32 [N]; NULL: row
+ * t) and attends to N(pos[t]) of graph g, its own key and value stored
+ * already: several tokens of one request may be decoded in one call.
+ * pos[t] = -1 marks a padded token: out = 0, lse = -inf.  The same happens,
+ * and the device error word is flagged, when pos[t] < -1 or not below
+ * min(g's T, max_pages * page_size), or row[t] is outside [0, rows).  A key
+ * whose block-table entry is outside [0, n_pages) is left out of the softmax
+ * and flagged.  Cache rows outside N(pos[t]) are never used, whatever they
+ * hold.  A row whose scores are all -inf gives out = 0, lse = -inf.  lse:
+ * fp32 [N, H].  Long rows are cut into shares for the whole GPU and joined
+ * by a second kernel in a fixed order: results do not change from run to
+ * run.  workspace: caller-owned, 256-byte aligned, contents don't matter
+ * before and after; calls that overlap on the GPU need their own. */
+sa_status sparse_attn_paged_decode(const sa_tensor *q, const sa_paged_cache *cache,
+                                   const int32_t *block_table, int64_t rows, int64_t max_pages,
+                                   const int32_t *row, const int64_t *pos, sa_graph g, float scale,
+                                   sa_tensor *out, float *lse, void *workspace, size_t ws_bytes,
+                                   void *stream);
 
 /* -------------------------------------------- learned-coordinate scoring */
 

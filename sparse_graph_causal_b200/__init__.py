@@ -19,13 +19,30 @@ LIB_PATH = os.path.join(_HERE, "libsparse_attn.so")
 
 SA_OK, SA_ERR_INVALID_ARG, SA_ERR_INVALID_GRAPH, SA_ERR_UNSUPPORTED = 0, 1, 2, 3
 SA_ERR_OOM, SA_ERR_CUDA, SA_ERR_DEVICE_TIMEOUT = 4, 5, 6
-SA_BF16, SA_FP32 = 0, 1
+SA_BF16, SA_FP32, SA_E4M3 = 0, 1, 2
+SA_PAGED_OK, SA_PAGED_NO_PAGES, SA_PAGED_REFUSED = 0, 1, 2
+SA_PAGED_MAX_REQUESTS = 8192
 SA_PATH_AUTO, SA_PATH_GATHER = 0, 1
 SA_LINKS_AUTO, SA_LINKS_SPLIT, SA_LINKS_ONE_PASS = 0, 1, 2
 
 class SaTensor(ctypes.Structure):
     _fields_ = [("ptr", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("B", ctypes.c_int64),
                 ("H", ctypes.c_int64), ("T", ctypes.c_int64), ("D", ctypes.c_int64)]
+
+
+class SaPagedCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("n_pages", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("D", ctypes.c_int64)]
+
+
+class SaPagedStep(ctypes.Structure):
+    _fields_ = ([(n, ctypes.c_int64) for n in ("B", "max_pages", "page_size", "capacity",
+                                               "n_stack")]
+                + [(n, ctypes.c_void_p) for n in ("len", "n_new", "block_table", "free_pages",
+                                                  "free_count", "len_out", "free_count_out",
+                                                  "cu_new", "slot", "pos", "row", "status")])
 
 
 def _load():
@@ -58,6 +75,14 @@ def _load():
                                          P(SaTensor), P(SaTensor), vp]),
         "sparse_attn_decode": (st, [P(SaTensor), P(SaTensor), P(SaTensor), vp, vp,
                                     ctypes.c_float, P(SaTensor), vp, vp]),
+        "sparse_attn_paged_plan": (st, [P(SaPagedStep), vp]),
+        "sparse_attn_paged_append": (st, [P(SaTensor), i64, P(SaTensor), i64, vp,
+                                          P(SaPagedCache), vp]),
+        "sparse_attn_paged_decode_workspace_size": (ctypes.c_size_t, [P(SaTensor),
+                                                                      P(SaPagedCache), vp]),
+        "sparse_attn_paged_decode": (st, [P(SaTensor), P(SaPagedCache), vp, i64, i64, vp, vp, vp,
+                                          ctypes.c_float, P(SaTensor), vp, vp, ctypes.c_size_t,
+                                          vp]),
         "sparse_attn_dist_fwd": (st, [P(SaTensor), P(SaTensor), P(SaTensor), vp,
                                       ctypes.c_float, P(SaTensor), vp, vp]),
         "sparse_attn_dist_bwd_workspace_size": (ctypes.c_size_t, [P(SaTensor), vp]),
@@ -301,6 +326,174 @@ def sparse_attn_decode(q, k_cache, v_cache, pos, g: Graph, scale: float, out=Non
     return out, lse
 
 
+# ------------------------------------------------------------- paged cache
+
+_PAGED_DTYPES = {torch.bfloat16: SA_BF16, torch.float32: SA_FP32, torch.float8_e4m3fn: SA_E4M3}
+
+
+def _array(t, name: str, dtype, shape, device):
+    """Address of a contiguous tensor of this type and shape on this device."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
+            or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
+                         f"on {device}")
+    return t.data_ptr()
+
+
+def _call_on(device, stream, call):
+    """call(stream) with the tensors' device current (the library launches on
+    the current one), on its current stream unless one is given."""
+    if device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+class PagedCache:
+    """Key and value pages [n_pages, Hkv, page_size, D] (bf16, fp32, or
+    float8_e4m3fn with fp32 scales [n_pages, Hkv, page_size]) of one layer."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if not isinstance(k, torch.Tensor) or not k.is_cuda or k.dim() != 4 \
+                or k.dtype not in _PAGED_DTYPES:
+            raise ValueError("k must be a CUDA [n_pages, Hkv, page_size, D] tensor in bf16, fp32 "
+                             "or float8_e4m3fn")
+        kp, vp = (_array(x, n, k.dtype, k.shape, k.device) for x, n in ((k, "k"), (v, "v")))
+        ks = vs = None
+        if k.dtype is torch.float8_e4m3fn:
+            ks, vs = (_array(x, n, torch.float32, k.shape[:3], k.device)
+                      for x, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
+        elif k_scale is not None or v_scale is not None:
+            raise ValueError("only float8_e4m3fn pages have scales")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.device, self.page_size = k.device, k.shape[2]
+        n, h, p, d = k.shape
+        self._desc = SaPagedCache(kp, vp, ks, vs, _PAGED_DTYPES[k.dtype], n, h, p, d)
+
+
+class PagedBatch:
+    """The tokens of one step, as sparse_attn_paged_plan writes them: cu_new
+    int64 [B + 1], slot and pos int64 [capacity], row int32 [capacity], status
+    int32 [B] (SA_PAGED_OK, SA_PAGED_NO_PAGES or SA_PAGED_REFUSED)."""
+
+    def __init__(self, B: int, capacity: int, device=None):
+        device = device or torch.device("cuda", torch.cuda.current_device())
+        new = lambda n, dtype: torch.empty(n, dtype=dtype, device=device)  # noqa: E731
+        self.cu_new = new(B + 1, torch.int64)
+        self.slot, self.pos = new(capacity, torch.int64), new(capacity, torch.int64)
+        self.row, self.status = new(capacity, torch.int32), new(B, torch.int32)
+
+
+def sparse_attn_paged_plan(length, n_new, block_table, free_pages, free_count, page_size: int,
+                           batch: PagedBatch, length_out=None, free_count_out=None, stream=None):
+    """Plan one step of B requests: take the pages their new tokens need, give
+    back those of finished ones (n_new = -1) and write every token's slot,
+    position and row into `batch`.  length int64 [B]; n_new int32 [B];
+    block_table int32 [B, max_pages]; free_pages int32 [n] a stack of
+    free_count (int64 [1]) pages.  block_table and free_pages are updated in
+    place, and so are length and free_count unless length_out and
+    free_count_out are given.  Returns batch."""
+    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda \
+            or block_table.dim() != 2:
+        raise ValueError("block_table must be a CUDA int32 [B, max_pages] tensor")
+    dev, (B, M) = block_table.device, block_table.shape
+    length_out = length if length_out is None else length_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    i64, i32, cap = torch.int64, torch.int32, batch.slot.numel()
+    d = SaPagedStep(
+        B, M, int(page_size), cap, free_pages.numel(),
+        _array(length, "length", i64, (B,), dev), _array(n_new, "n_new", i32, (B,), dev),
+        _array(block_table, "block_table", i32, (B, M), dev),
+        _array(free_pages, "free_pages", i32, (free_pages.numel(),), dev),
+        _array(free_count, "free_count", i64, (1,), dev),
+        _array(length_out, "length_out", i64, (B,), dev),
+        _array(free_count_out, "free_count_out", i64, (1,), dev),
+        _array(batch.cu_new, "cu_new", i64, (B + 1,), dev),
+        _array(batch.slot, "slot", i64, (cap,), dev), _array(batch.pos, "pos", i64, (cap,), dev),
+        _array(batch.row, "row", i32, (cap,), dev), _array(batch.status, "status", i32, (B,), dev))
+    _check(_call_on(dev, stream, lambda s: _lib.sparse_attn_paged_plan(ctypes.byref(d), s)),
+           "sparse_attn_paged_plan")
+    return batch
+
+
+def _token_rows(t, name: str, cache: PagedCache):
+    """New rows [N, Hkv, D] or [N, Hkv, 1, D] with any stride between tokens:
+    the descriptor and that stride."""
+    c = cache._desc
+    if not isinstance(t, torch.Tensor) or t.device != cache.device:
+        raise ValueError(f"{name} must be a tensor on {cache.device}")
+    if t.dim() == 4 and t.shape[2] == 1:
+        t = t[:, :, 0]
+    if t.dim() != 3 or t.shape[1:] != (c.Hkv, c.D) or t.stride(2) != 1 \
+            or (c.Hkv > 1 and t.stride(1) != c.D):
+        raise ValueError(f"{name} must be [N, {c.Hkv}, {c.D}] with contiguous heads")
+    dt = _PAGED_DTYPES.get(t.dtype, -1)
+    if dt == SA_E4M3:
+        raise ValueError(f"{name}: new rows are bf16 or fp32")
+    stride = t.stride(0) if t.shape[0] > 1 else c.Hkv * c.D
+    return SaTensor(t.data_ptr(), dt, t.shape[0], c.Hkv, 1, c.D), stride
+
+
+def sparse_attn_paged_append(k_new, v_new, cache: PagedCache, slot, stream=None):
+    """Write rows k_new, v_new [N, Hkv, D] (or [N, Hkv, 1, D]; the stride
+    between tokens is free) to the cache rows slot int64 [N]; negative slots
+    are skipped.  bf16 rows are rounded to 8 bits, one scale per row, for a
+    float8_e4m3fn cache."""
+    (tk, sk), (tv, sv) = _token_rows(k_new, "k_new", cache), _token_rows(v_new, "v_new", cache)
+    if tk.B == 0 and tv.B == 0:
+        return
+    ps = _array(slot, "slot", torch.int64, (tk.B,), cache.device)
+    _check(_call_on(cache.device, stream,
+                    lambda s: _lib.sparse_attn_paged_append(
+                        ctypes.byref(tk), sk, ctypes.byref(tv), sv, ps,
+                        ctypes.byref(cache._desc), s)),
+           "sparse_attn_paged_append")
+
+
+def sparse_attn_paged_decode_workspace_size(q, cache: PagedCache, g: Graph) -> int:
+    tq = _tensor(q, "q")
+    return int(_lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(tq),
+                                                            ctypes.byref(cache._desc), g.handle))
+
+
+def sparse_attn_paged_decode(q, cache: PagedCache, block_table, pos, g: Graph, scale: float,
+                             row=None, out=None, lse=None, workspace=None, stream=None):
+    """q [N, H, 1, D]: one query per new token, at position pos (int64 [N], -1
+    for a padded one) of the request in row `row` (int32 [N]; default: token
+    t's is row t) of block_table (int32 [rows, max_pages]).  Returns (out
+    [N, H, 1, D], lse fp32 [N, H])."""
+    tq = _tensor(q, "q")
+    N, H, _, D = q.shape
+    dev = cache.device
+    if q.device != dev:
+        raise ValueError(f"q must be on {dev}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be a CUDA int32 [rows, max_pages] tensor")
+    out = torch.empty_like(q) if out is None else out
+    if lse is None:
+        lse = torch.empty((N, H), dtype=torch.float32, device=dev)
+    if N == 0:
+        return out, lse
+    _array(out, "out", q.dtype, q.shape, dev)
+    _array(lse, "lse", torch.float32, (N, H), dev)
+    _array(block_table, "block_table", torch.int32, block_table.shape, dev)
+    _array(pos, "pos", torch.int64, (N,), dev)
+    if row is not None:
+        _array(row, "row", torch.int32, (N,), dev)
+    if workspace is None:
+        n = sparse_attn_paged_decode_workspace_size(q, cache, g)
+        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
+    to = SaTensor(out.data_ptr(), tq.dtype, N, H, 1, D)
+    _check(_call_on(dev, stream, lambda s: _lib.sparse_attn_paged_decode(
+        ctypes.byref(tq), ctypes.byref(cache._desc), block_table.data_ptr(),
+        block_table.shape[0], block_table.shape[1], None if row is None else row.data_ptr(),
+        pos.data_ptr(), g.handle, float(scale), ctypes.byref(to), lse.data_ptr(),
+        None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), s)),
+        "sparse_attn_paged_decode")
+    return out, lse
+
+
 # ------------------------------------------------ learned-coordinate scoring
 
 def _coords(t: torch.Tensor, name: str) -> SaTensor:
@@ -458,4 +651,4 @@ def attention(q, k, v, graph: Graph, scale: float):
 
 
 __all__ = [n for n in dir() if n.startswith("sparse_attn_")] + [
-    "Graph", "attention", "dist_attention", "SparseAttentionError", "LIB_PATH"]
+    "Graph", "PagedBatch", "PagedCache", "attention", "dist_attention", "SparseAttentionError", "LIB_PATH"]

@@ -549,3 +549,109 @@ extern "C" sa_status sparse_attn_decode(const sa_tensor *q, const sa_tensor *k_c
     if (dev != g->device) return SA_ERR_INVALID_ARG;
     return sa_decode(q, k_cache, v_cache, pos, make_view(g), scale, out, lse, as_stream(stream));
 }
+
+// ------------------------------------------------------------- paged cache
+
+namespace {
+
+constexpr int64_t kInt32Max = 0x7fffffffLL;
+
+bool aligned(const void *p, unsigned a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool array_ok(const void *p, unsigned a) { return p && aligned(p, a); }
+
+sa_status check_paged_cache(const sa_paged_cache *c) {
+    if (!c || !array_ok(c->k, 16) || !array_ok(c->v, 16)) return SA_ERR_INVALID_ARG;
+    if (c->dtype != SA_BF16 && c->dtype != SA_FP32 && c->dtype != SA_E4M3)
+        return SA_ERR_INVALID_ARG;
+    if (c->n_pages < 1 || c->Hkv < 1 || c->page_size < 1 || c->D < 1) return SA_ERR_INVALID_ARG;
+    if (c->dtype == SA_E4M3 ? !array_ok(c->k_scale, 4) || !array_ok(c->v_scale, 4)
+                            : c->k_scale || c->v_scale)
+        return SA_ERR_INVALID_ARG;
+    if (c->D != 32 && c->D != 64 && c->D != 128) return SA_ERR_UNSUPPORTED;
+    if (c->n_pages > kInt32Max || c->page_size > kInt32Max || c->Hkv > kInt32Max)
+        return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+// New rows or queries of a call on cache c: [N, heads, 1, D].
+sa_status check_paged_rows(const sa_tensor *t, const sa_paged_cache *c) {
+    sa_status st = check_tensor(t, nullptr);
+    if (st != SA_OK) return st;
+    if (t->T != 1 || t->D != c->D || t->dtype != (c->dtype == SA_E4M3 ? SA_BF16 : c->dtype))
+        return SA_ERR_INVALID_ARG;
+    if (t->B > kInt32Max) return SA_ERR_UNSUPPORTED;
+    return SA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+sa_status sparse_attn_paged_plan(const sa_paged_step *p, void *stream) {
+    if (!p) return SA_ERR_INVALID_ARG;
+    if (p->B < 1 || p->max_pages < 1 || p->page_size < 1 || p->capacity < 1 || p->n_stack < 1)
+        return SA_ERR_INVALID_ARG;
+    const void *wide[] = {p->len,    p->free_count, p->len_out, p->free_count_out,
+                          p->cu_new, p->slot,       p->pos};
+    for (const void *a : wide)
+        if (!array_ok(a, 8)) return SA_ERR_INVALID_ARG;
+    const void *narrow[] = {p->n_new, p->block_table, p->free_pages, p->row, p->status};
+    for (const void *a : narrow)
+        if (!array_ok(a, 4)) return SA_ERR_INVALID_ARG;
+    if (p->B > SA_PAGED_MAX_REQUESTS || p->capacity > kInt32Max || p->n_stack > kInt32Max ||
+        p->page_size > kInt32Max || p->max_pages > kInt32Max / p->page_size)
+        return SA_ERR_UNSUPPORTED;
+    return sa_paged_plan(*p, as_stream(stream));
+}
+
+sa_status sparse_attn_paged_append(const sa_tensor *k_new, int64_t k_stride,
+                                   const sa_tensor *v_new, int64_t v_stride, const int64_t *slot,
+                                   const sa_paged_cache *cache, void *stream) {
+    sa_status st = check_paged_cache(cache);
+    if (st != SA_OK) return st;
+    if ((st = check_paged_rows(k_new, cache)) != SA_OK ||
+        (st = check_tensor(v_new, k_new)) != SA_OK)
+        return st;
+    if (k_new->H != cache->Hkv || !array_ok(slot, 8)) return SA_ERR_INVALID_ARG;
+    const int64_t unit = k_new->dtype == SA_BF16 ? 8 : 4;  // elements of 16 bytes
+    const int64_t strides[] = {k_stride, v_stride};
+    for (int64_t x : strides)
+        if (x < cache->Hkv * cache->D || x % unit != 0) return SA_ERR_INVALID_ARG;
+    return sa_paged_append(k_new, k_stride, v_new, v_stride, slot, *cache, as_stream(stream));
+}
+
+size_t sparse_attn_paged_decode_workspace_size(const sa_tensor *q, const sa_paged_cache *cache,
+                                               sa_graph g) {
+    if (!g || check_paged_cache(cache) != SA_OK || check_paged_rows(q, cache) != SA_OK ||
+        q->H % cache->Hkv != 0)
+        return 0;
+    return sa_paged_decode_workspace(q, *cache, g);
+}
+
+sa_status sparse_attn_paged_decode(const sa_tensor *q, const sa_paged_cache *cache,
+                                   const int32_t *block_table, int64_t rows, int64_t max_pages,
+                                   const int32_t *row, const int64_t *pos, sa_graph g, float scale,
+                                   sa_tensor *out, float *lse, void *workspace, size_t ws_bytes,
+                                   void *stream) {
+    if (!g) return SA_ERR_INVALID_ARG;
+    sa_status st = check_paged_cache(cache);
+    if (st != SA_OK) return st;
+    if ((st = check_paged_rows(q, cache)) != SA_OK || (st = check_tensor(out, q)) != SA_OK)
+        return st;
+    if (q->H % cache->Hkv != 0 || rows < 1 || max_pages < 1) return SA_ERR_INVALID_ARG;
+    if (!array_ok(block_table, 4) || !array_ok(pos, 8) || !aligned(row, 4) ||
+        !array_ok(lse, 16) || !std::isfinite(scale))
+        return SA_ERR_INVALID_ARG;
+    if (!row && rows < q->B) return SA_ERR_INVALID_ARG;
+    if (rows > kInt32Max || max_pages > kInt32Max / cache->page_size) return SA_ERR_UNSUPPORTED;
+    const size_t need = sa_paged_decode_workspace(q, *cache, g);
+    if (need && (!array_ok(workspace, 256) || ws_bytes < need)) return SA_ERR_INVALID_ARG;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return SA_ERR_CUDA;
+    if (dev != g->device) return SA_ERR_INVALID_ARG;
+    return sa_paged_decode(q, *cache, block_table, rows, max_pages, row, pos, g, scale, out, lse,
+                           workspace, as_stream(stream));
+}
+
+}  // extern "C"

@@ -193,3 +193,15 @@ sa_status sa_dist_bwd(const sa_tensor *a, const sa_tensor *c, const sa_tensor *v
 sa_status sa_decode(const sa_tensor *q, const sa_tensor *k, const sa_tensor *v,
                     const int64_t *pos, const GraphView &g, float scale, sa_tensor *out,
                     float *lse, cudaStream_t s);
+
+// Internal launchers of the paged cache (paged_plan.cu, paged_append.cu,
+// paged_decode.cu); the arguments are checked already.
+sa_status sa_paged_plan(const sa_paged_step &p, cudaStream_t s);
+sa_status sa_paged_append(const sa_tensor *k, int64_t k_stride, const sa_tensor *v,
+                          int64_t v_stride, const int64_t *slot, const sa_paged_cache &c,
+                          cudaStream_t s);
+size_t sa_paged_decode_workspace(const sa_tensor *q, const sa_paged_cache &c, const sa_graph_s *g);
+sa_status sa_paged_decode(const sa_tensor *q, const sa_paged_cache &c, const int32_t *table,
+                          int64_t rows, int64_t max_pages, const int32_t *row, const int64_t *pos,
+                          const sa_graph_s *g, float scale, sa_tensor *out, float *lse,
+                          void *workspace, cudaStream_t s);
