@@ -644,7 +644,7 @@ sa_status sparse_attn_paged_decode(const sa_tensor *q, const sa_paged_cache *cac
         !array_ok(lse, 16) || !std::isfinite(scale))
         return SA_ERR_INVALID_ARG;
     if (!row && rows < q->B) return SA_ERR_INVALID_ARG;
-    if (rows > kInt32Max || max_pages > kInt32Max / cache->page_size) return SA_ERR_UNSUPPORTED;
+    if (rows > kInt32Max || max_pages > (1LL << 30) / cache->page_size) return SA_ERR_UNSUPPORTED;
     const size_t need = sa_paged_decode_workspace(q, *cache, g);
     if (need && (!array_ok(workspace, 256) || ws_bytes < need)) return SA_ERR_INVALID_ARG;
     int dev = 0;

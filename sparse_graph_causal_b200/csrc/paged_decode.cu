@@ -1,13 +1,52 @@
 // paged_decode.cu -- attention of new tokens over the sparse graph, keys and
-// values in the pages of a cache.
+// values in the pages of a cache:
+//     out = sum_j p_j v_j / sum_j p_j,   p_j = exp(scale q . k_j),  j in N(pos)
 //
-// One CTA per (token, query head): groups of lanes hold one cached row each
-// (16 bytes per lane), every group has its own online-softmax state, merged
-// by shuffles and then across the warps in shared memory.
+// Bound: every key and value row of a (token, cache head) is read once, by all
+// query heads of its group together, so the work is HBM traffic: 2 D es bytes
+// for 4 G D operations, G query heads to a cache head.  Everything below is
+// there to keep the loads in flight.
+//
+// A warp owns a run of one row's edges and gathers them tile by tile with
+// cp.async: rows are addressed one by one (edge -> position -> page -> cache
+// row), so that windows, distance links, CSR lists and pages of any size go
+// the same way.  A ring of stages per warp holds the tiles in flight; the
+// positions and pages of later tiles are fetched ahead of their copies.
+//
+// 16-bit and 8-bit caches: mma.sync m16n8k16, S = Q K^T and O += P V, with
+// eight (or sixteen) query heads as rows.  The tensor work is a fifth of the
+// time that the bytes take, so the shape wastes nothing that counts, and the
+// warp needs no other warp.  The sums over d (of S) and the columns (of O) may
+// be taken in any order, so a lane's fragment is whatever 16 bytes of a row it
+// can load at once: each lane copies the very bytes that it multiplies, and
+// the stages are its own storage, without bank conflicts or a layout.
+//   S: lane (g, t) = (lane / 4, lane % 4) holds 16-byte pieces t, t + 4, ... of
+//      key g;  O: pieces g, g + 8, ... of the value rows 2t, 2t+1, 2t+8, 2t+9.
+// P has 16 bits in the product; with one 8-head block the lower eight rows of
+// the tile are free and carry what the rounding of P left over (P = hi + lo, 2^-17),
+// so that probabilities are as good as 32-bit ones at no cost.
+//   8-bit rows become fp16 exactly.  A query row is scaled by a power of two
+// into fp16's range; a value row's scale goes into its weight, and the weights
+// have a running maximum of their own, so that no choice of scales overflows or
+// loses them.
+//
+// fp32 caches: CUDA cores, a lane per key for the scores, a lane per four
+// columns for the values, both from the staged tile.
+//
+// Two ways to share the work:
+//   direct  rows that the graph keeps short: a CTA per (token, cache head), its
+//           warps take equal runs and merge in shared memory.
+//   split   the tiles of all rows, end to end, are cut into equal runs for all
+//           warps of the GPU, wherever rows begin or end.  Whole rows are
+//           finished by their warp; rows that are cut leave (m, l, acc), merged
+//           first by the CTA and then, across CTAs, by a second small kernel.
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "gather_common.cuh"
 
@@ -15,170 +54,1068 @@ namespace {
 
 using namespace gather;
 
-constexpr int kWarps = 8;
+constexpr unsigned kFull = 0xffffffffu;
+
+// ------------------------------------------------------------------ pieces
+
+// n / P for 0 <= n < 2^31 as a product: with 2^(l-1) < P <= 2^l, M = ceil(2^(31+l) / P)
+// overshoots by e < P <= 2^l parts in 2^(31+l), and n e < 2^(31+l).
+struct Divide {
+    uint32_t mul, shift, by;
+};
+
+Divide make_divide(uint32_t by) {
+    uint32_t l = 0;
+    while ((1ull << l) < by) ++l;
+    const unsigned __int128 one = (unsigned __int128)1 << (31 + l);
+    return {(uint32_t)((one + by - 1) / by), 31 + l, by};
+}
+
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divide &d) {
+    return (uint32_t)(((uint64_t)n * d.mul) >> d.shift);
+}
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return (uint32_t)__cvta_generic_to_shared(p);
+}
+
+// Copies of 4, 8 or 16 bytes; with `on` false the bytes are set to zero and
+// nothing is read.
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool on) {
+    const int n = on ? B : 0;
+    if constexpr (B == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n)
+                     : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(B),
+                     "r"(n)
+                     : "memory");
+}
+
+__device__ __forceinline__ void copies_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <int B>
+__device__ __forceinline__ void load_words(uint32_t *w, const void *p) {
+    if constexpr (B == 16) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (B == 8) {
+        const uint2 x = *reinterpret_cast<const uint2 *>(p);
+        w[0] = x.x, w[1] = x.y;
+    } else {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    }
+}
+
+struct E4m3 {
+    uint8_t x;
+};
+
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1, __nv_bfloat16) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                    uint32_t b1, E4m3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t half_bits(__half2 h) {
+    return *reinterpret_cast<uint32_t *>(&h);
+}
+
+// Two 8-bit values as two fp16 ones (exact).
+__device__ __forceinline__ uint32_t widen(uint32_t two) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
+    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+}
+
+// p0, p1 as 16-bit numbers and what their rounding leaves.
+__device__ __forceinline__ void split16(float p0, float p1, uint32_t &hi, uint32_t &lo,
+                                        __nv_bfloat16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(p0, p1);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    const __nv_bfloat162 r = __floats2bfloat162_rn(p0 - __uint_as_float(hi << 16),
+                                                   p1 - __uint_as_float(hi & 0xffff0000u));
+    lo = *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ void split16(float p0, float p1, uint32_t &hi, uint32_t &lo, E4m3) {
+    const __half2 h = __floats2half2_rn(p0, p1);
+    const float2 f = __half22float2(h);
+    hi = half_bits(h);
+    lo = half_bits(__floats2half2_rn(p0 - f.x, p1 - f.y));
+}
+
+__device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
+
+// --------------------------------------------------------------- arguments
 
 struct DecodeArgs {
     const void *q, *k, *v;
     const float *k_scale, *v_scale;
     const int32_t *table, *row;
     const int64_t *pos;
-    int64_t rows, max_pages, n_pages;
-    int32_t H, Hkv, P;
-    float scale2;
+    int64_t N, rows, max_pages, n_pages;
+    int32_t H, Hkv, G, QB;  // query heads, cache heads, their ratio, blocks of it
+    Divide page;
+    float scale2;           // scale * log2(e)
     void *out;
     float *lse;
+    float *warp_part, *cta_part;  // slots [warp or CTA][2] of partial rows
+    int4 *cut;                    // per CTA: the row that starts there and is cut
     int *err;
 };
 
-struct E4m3 {
-    uint8_t x;
+// One token's row of edges.
+struct Token {
+    int64_t p;
+    RowEdges e;
+    const int32_t *pages;
+    int32_t deg;
+    bool bad;
 };
 
-template <typename T>
-struct Row {
-    using Q = T;
-    static constexpr int V = Slice<T>::V;
-    __device__ static void load(const void *p, int64_t at, float *f) {
-        Slice<T>::load((const T *)p + at, f);
+__device__ __forceinline__ Token token_of(const DecodeArgs &a, const GraphView &g, int64_t n) {
+    Token t;
+    t.p = a.pos[n];
+    const int64_t r = a.row ? a.row[n] : n;
+    const bool ok = t.p >= 0 && t.p < g.T && t.p < a.max_pages * a.page.by && r >= 0 && r < a.rows;
+    t.bad = !ok && t.p != -1;
+    t.deg = 0;
+    t.pages = a.table;
+    t.e = RowEdges{};
+    if (ok) {
+        t.e = row_edges(g, t.p);
+        t.deg = (int32_t)t.e.deg;
+        t.pages = a.table + r * a.max_pages;
     }
-};
-template <>
-struct Row<E4m3> {
-    using Q = __nv_bfloat16;
-    static constexpr int V = 8;
-    __device__ static void load(const void *p, int64_t at, float *f) {
-        const __nv_fp8x4_e4m3 *x = (const __nv_fp8x4_e4m3 *)((const uint8_t *)p + at);
-#pragma unroll
-        for (int a = 0; a < 2; ++a) {
-            const float4 y = (float4)x[a];
-            f[4 * a] = y.x;
-            f[4 * a + 1] = y.y;
-            f[4 * a + 2] = y.z;
-            f[4 * a + 3] = y.w;
-        }
-    }
+    return t;
+}
+
+// A partial row: m[NQ], l[NQ], acc[NQ][D].
+template <int NQ, int D>
+struct Part {
+    static constexpr int kFloats = NQ * (D + 2);
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(32 * kWarps) paged_decode_kernel(DecodeArgs a, GraphView g) {
-    using Q = typename Row<T>::Q;
-    constexpr int V = Row<T>::V, L = D / V, G = 32 / L;
-    constexpr int NG = G * kWarps;
-    __shared__ float s_m[kWarps], s_l[kWarps];
-    __shared__ float s_acc[kWarps][D];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int grp = lane / L, sub = lane % L;
-    const int64_t nh = blockIdx.x, n = nh / a.H, h = nh % a.H;
-    const int64_t kvh = h / (a.H / a.Hkv);
-    const int64_t p = a.pos[n], r = a.row ? a.row[n] : n;
-    const bool ok = p >= 0 && p < g.T && p < a.max_pages * a.P && r >= 0 && r < a.rows;
-    Q *out = (Q *)a.out;
-    if (!ok) {
-        if (threadIdx.x == 0) {
-            if (p != -1) atomicOr(a.err, SA_DEVERR_BOUNDS);
-            a.lse[nh] = -INFINITY;
-        }
-        if (threadIdx.x < D) out[nh * D + threadIdx.x] = Q(0.f);
-        return;
-    }
-    float qf[V];
-#pragma unroll
-    for (int x = 0; x < V; ++x) qf[x] = (float)((const Q *)a.q)[nh * D + sub * V + x] * a.scale2;
-    const RowEdges e = row_edges(g, p);
-    float m = -INFINITY, l = 0.f, acc[V];
-#pragma unroll
-    for (int x = 0; x < V; ++x) acc[x] = 0.f;
-    for (int64_t e0 = 0; e0 < e.deg; e0 += NG) {
-        const int64_t x0 = e0 + warp * G + grp;
-        bool valid = x0 < e.deg;
-        float kf[V], vf[V], ks = 1.f, vs = 1.f;
-#pragma unroll
-        for (int x = 0; x < V; ++x) kf[x] = vf[x] = 0.f;
-        if (valid) {
-            const int64_t j = row_edge(g, e, p, x0);
-            const int64_t page = a.table[r * a.max_pages + j / a.P];
-            if (page < 0 || page >= a.n_pages) {
-                valid = false;
-                if (sub == 0) atomicOr(a.err, SA_DEVERR_BOUNDS);
-            } else {
-                const int64_t at = (page * a.Hkv + kvh) * a.P + j % a.P;
-                Row<T>::load(a.k, at * D + sub * V, kf);
-                Row<T>::load(a.v, at * D + sub * V, vf);
-                if (a.k_scale) {
-                    ks = a.k_scale[at];
-                    vs = a.v_scale[at];
-                }
-            }
-        }
-        float s = 0.f;
-#pragma unroll
-        for (int x = 0; x < V; ++x) s = fmaf(qf[x], kf[x], s);
-        s = group_sum<L>(s) * ks;
-        if (valid) {
-            const float mn = fmaxf(m, s);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            const float al = ex2(m - base), pe = ex2(s - base);
-            l = l * al + pe;
-#pragma unroll
-            for (int x = 0; x < V; ++x) acc[x] = fmaf(pe * vs, vf[x], acc[x] * al);
-            m = mn;
-        }
-    }
-#pragma unroll
-    for (int o = L; o < 32; o <<= 1) {
-        const float mo = __shfl_xor_sync(0xffffffffu, m, o);
-        const float lo = __shfl_xor_sync(0xffffffffu, l, o);
-        const float mn = fmaxf(m, mo), base = mn == -INFINITY ? 0.f : mn;
-        const float w0 = ex2(m - base), w1 = ex2(mo - base);
-        l = l * w0 + lo * w1;
-#pragma unroll
-        for (int x = 0; x < V; ++x)
-            acc[x] = acc[x] * w0 + __shfl_xor_sync(0xffffffffu, acc[x], o) * w1;
+// Joins two softmax states.
+struct State {
+    float m = -INFINITY, l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    __device__ __forceinline__ void add(float m1, float l1, float4 o1) {
+        const float mn = fmaxf(m, m1), base = finite_base(mn);
+        const float w0 = ex2(m - base), w1 = ex2(m1 - base);
+        l = l * w0 + l1 * w1;
+        o.x = o.x * w0 + o1.x * w1;
+        o.y = o.y * w0 + o1.y * w1;
+        o.z = o.z * w0 + o1.z * w1;
+        o.w = o.w * w0 + o1.w * w1;
         m = mn;
     }
-    if (grp == 0) {
+    __device__ __forceinline__ float lse() const {
+        return l == 0.f ? -INFINITY : (finite_base(m) + lg2(l)) * kLn2;
+    }
+};
+
+__device__ __forceinline__ float4 divided(float4 o, float l) {
+    if (l == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(o.x / l, o.y / l, o.z / l, o.w / l);
+}
+
+__device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 o) {
+    const __nv_bfloat162 x = __floats2bfloat162_rn(o.x, o.y), y = __floats2bfloat162_rn(o.z, o.w);
+    *reinterpret_cast<uint2 *>(p) = make_uint2(*reinterpret_cast<const uint32_t *>(&x),
+                                               *reinterpret_cast<const uint32_t *>(&y));
+}
+__device__ __forceinline__ void store4(float *p, float4 o) { *reinterpret_cast<float4 *>(p) = o; }
+
+// ------------------------------------------------- 16-bit and 8-bit tiles
+
+// One warp's work on tiles of KT keys.  NB: blocks of eight query heads.
+template <typename T, int kD, int NB>
+struct MmaTile {
+    using Out = __nv_bfloat16;
+    static constexpr bool k8 = sizeof(T) == 1;
+    static constexpr int D = kD, NQ = 8 * NB;
+    static constexpr int RB = D * (int)sizeof(T);          // bytes of a row
+    static constexpr int KT = RB == 256 || (!k8 && D == 64) ? 16 : 32;
+    static constexpr int kStages = RB == 32 ? 4 : 3, kWarps = 8;
+    static constexpr int kOcc = D == 128 || NB == 2 ? 1 : 2;
+    static constexpr int KP = RB / 4 < 16 ? RB / 4 : 16, KN = RB / 4 / KP;
+    static constexpr int VP = RB / 8 < 16 ? RB / 8 : 16, VN = RB / 8 / VP;
+    static constexpr int VE = VP / (int)sizeof(T);
+    static constexpr int kScaleBytes = k8 ? 2 * KT * 4 : 0;
+    static constexpr int kStageBytes = 2 * KT * RB + kScaleBytes;
+    static constexpr int kOwnBytes = 0;  // beyond the stages
+    static constexpr int KS = D / 16, NT = D / 8;
+
+    int lane, g, t;
+    uint32_t qf[KS][NB == 1 ? 2 : 4];
+    float unit[NB];  // of a score, in base 2
+    float m[NB], l[NB];
+    float mw[NB];    // running maximum of the weights (8-bit values)
+    float acc[NB][NT][4];
+
+    __device__ __forceinline__ void begin(const DecodeArgs &a, void *, int64_t n, int64_t h0,
+                                          int gq) {
+        lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+        constexpr int KE = KP / (int)sizeof(T);
 #pragma unroll
-        for (int x = 0; x < V; ++x) s_acc[warp][sub * V + x] = acc[x];
-        if (sub == 0) {
-            s_m[warp] = m;
-            s_l[warp] = l;
+        for (int b = 0; b < NB; ++b) {
+            const bool on = b * 8 + g < gq;
+            const uint8_t *q = (const uint8_t *)a.q + 2 * D * (n * a.H + h0 + (on ? b * 8 + g : 0));
+            uint32_t w[D / 8];
+#pragma unroll
+            for (int x = 0; x < D / 8; x += 4) {
+                const int e = 2 * x;  // element within the lane's D / 4
+                const uint4 u = *reinterpret_cast<const uint4 *>(
+                    q + 2 * ((e / KE * 4 + t) * KE + e % KE));
+                w[x] = on ? u.x : 0, w[x + 1] = on ? u.y : 0;
+                w[x + 2] = on ? u.z : 0, w[x + 3] = on ? u.w : 0;
+            }
+            unit[b] = a.scale2;
+            if constexpr (k8) {
+                uint32_t top = 0;
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+                    top = max(top, max((w[x] << 16) & 0x7fffffffu, w[x] & 0x7fff0000u));
+                top = max(top, __shfl_xor_sync(kFull, top, 1));
+                top = max(top, __shfl_xor_sync(kFull, top, 2));
+                // the row's largest magnitude to 2^14 .. 2^15; what falls below
+                // fp16's 2^-24 is 2^-39 of it
+                const int ex = max((int)(top >> 23) - 127, -100);
+                const float up = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
+                unit[b] *= __uint_as_float((uint32_t)(127 - 14 + ex) << 23);
+#pragma unroll
+                for (int x = 0; x < D / 8; ++x)
+                    w[x] = half_bits(__floats2half2_rn(__uint_as_float(w[x] << 16) * up,
+                                                       __uint_as_float(w[x] & 0xffff0000u) * up));
+            }
+#pragma unroll
+            for (int s = 0; s < KS; ++s) {
+                qf[s][b] = w[2 * s];
+                qf[s][NB + b] = w[2 * s + 1];
+            }
+            m[b] = mw[b] = -INFINITY;
+            l[b] = 0.f;
+#pragma unroll
+            for (int x = 0; x < NT; ++x)
+#pragma unroll
+                for (int y = 0; y < 4; ++y) acc[b][x][y] = 0.f;
         }
     }
-    __syncthreads();
-    if (threadIdx.x < D) {
-        float mt = -INFINITY, lt = 0.f, o = 0.f;
-        for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_m[w]);
-        const float base = mt == -INFINITY ? 0.f : mt;
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = ex2(s_m[w] - base);
-            lt = fmaf(s_l[w], f, lt);
-            o = fmaf(s_acc[w][threadIdx.x], f, o);
+
+    // Start the copies of a tile: rows[] are the cache rows of its keys, -1 for none.
+    __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage,
+                                         const int64_t *rows) const {
+        const uint32_t dst = smem_addr(stage) + (threadIdx.x & 31) * KP;
+        const int ln = threadIdx.x & 31, gg = ln >> 2, tt = ln & 3;
+#pragma unroll
+        for (int x = 0; x < KT / 8; ++x) {
+            const int64_t r = rows[x * 8 + gg];
+            const uint8_t *src = (const uint8_t *)a.k + (r < 0 ? 0 : r) * RB + tt * KP;
+#pragma unroll
+            for (int i = 0; i < KN; ++i)
+                copy_async<KP>(dst + (x * KN + i) * 32 * KP, src + i * 4 * KP, r >= 0);
         }
-        out[nh * D + threadIdx.x] = Q(lt == 0.f ? 0.f : o / lt);
-        if (threadIdx.x == 0) a.lse[nh] = lt == 0.f ? -INFINITY : (base + lg2(lt)) * kLn2;
+        const uint32_t vdst = smem_addr(stage) + KT * RB + ln * VP;
+#pragma unroll
+        for (int x = 0; x < KT / 4; ++x) {
+            const int64_t r = rows[x / 4 * 16 + (x & 2) * 4 + 2 * tt + (x & 1)];
+            const uint8_t *src = (const uint8_t *)a.v + (r < 0 ? 0 : r) * RB + gg * VP;
+#pragma unroll
+            for (int i = 0; i < VN; ++i)
+                copy_async<VP>(vdst + (x * VN + i) * 32 * VP, src + i * 8 * VP, r >= 0);
+        }
+        if constexpr (k8) {
+            const uint32_t sdst = smem_addr(stage) + 2 * KT * RB;
+#pragma unroll
+            for (int x = 0; x < 2 * KT; x += 32) {
+                const int at = x + ln, key = at % KT;
+                const int64_t r = rows[key];
+                copy_async<4>(sdst + 4 * at, (at < KT ? a.k_scale : a.v_scale) + (r < 0 ? 0 : r),
+                              r >= 0);
+            }
+        }
+    }
+
+    __device__ __forceinline__ void tile(const uint8_t *stage, uint32_t mask) {
+        constexpr int KB = KT / 8;
+        float s[KB][4];
+        const float *scales = reinterpret_cast<const float *>(stage + 2 * KT * RB);
+        // scores
+#pragma unroll
+        for (int x = 0; x < KB; ++x) {
+            s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+            uint32_t w[KN * KP / 4];
+#pragma unroll
+            for (int i = 0; i < KN; ++i)
+                load_words<KP>(w + i * KP / 4, stage + ((x * KN + i) * 32 + lane) * KP);
+#pragma unroll
+            for (int y = 0; y < KS; ++y) {
+                uint32_t qa[4];
+                qa[0] = qf[y][0];
+                qa[2] = qf[y][NB];
+                qa[1] = NB == 1 ? 0 : qf[y][NB - 1];
+                qa[3] = NB == 1 ? 0 : qf[y][2 * NB - 1];
+                if constexpr (k8)
+                    mma(s[x], qa, widen(w[y] & 0xffffu), widen(w[y] >> 16), T());
+                else
+                    mma(s[x], qa, w[2 * y], w[2 * y + 1], T());
+            }
+        }
+        uint32_t ph[NB][KB], pl[NB][KB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            float top = m[b], topw = mw[b];
+            float lv[KB][2];  // log2 of the value scales
+#pragma unroll
+            for (int x = 0; x < KB; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    const int key = x * 8 + 2 * t + y;
+                    float z = s[x][2 * b + y] * unit[b];
+                    if constexpr (k8) z *= scales[key];
+                    if (!((mask >> key) & 1)) z = -INFINITY;
+                    s[x][2 * b + y] = z;
+                    top = fmaxf(top, z);
+                    if constexpr (k8) {
+                        lv[x][y] = lg2(fabsf(scales[KT + key]));
+                        if (!((mask >> key) & 1)) lv[x][y] = 0.f;
+                        topw = fmaxf(topw, z + lv[x][y]);
+                    }
+                }
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
+            const float base = finite_base(top);
+            l[b] *= ex2(m[b] - base);
+            float old = m[b], now = base;
+            if constexpr (k8) {
+                topw = fmaxf(topw, __shfl_xor_sync(kFull, topw, 1));
+                topw = fmaxf(topw, __shfl_xor_sync(kFull, topw, 2));
+                old = mw[b];
+                now = finite_base(topw);
+                mw[b] = topw;
+            }
+            const float fall = ex2(old - now);
+            if (__any_sync(kFull, fall != 1.f)) {
+#pragma unroll
+                for (int x = 0; x < NT; ++x)
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) acc[b][x][y] *= fall;
+            }
+            m[b] = top;
+#pragma unroll
+            for (int x = 0; x < KB; ++x) {
+                const float z0 = s[x][2 * b], z1 = s[x][2 * b + 1];
+                float p0 = ex2(z0 - base), p1 = ex2(z1 - base);
+                l[b] += p0 + p1;
+                if constexpr (k8) {
+                    // up to 2^14, so that fp16's smallest step is 2^-38 of the largest
+                    const int key = x * 8 + 2 * t;
+                    p0 = copysignf(ex2(z0 + lv[x][0] - now + 14.f), scales[KT + key]);
+                    p1 = copysignf(ex2(z1 + lv[x][1] - now + 14.f), scales[KT + key + 1]);
+                }
+                split16(p0, p1, ph[b][x], pl[b][x], T());
+            }
+        }
+        // values
+#pragma unroll
+        for (int x = 0; x < KT / 16; ++x)
+#pragma unroll
+            for (int i = 0; i < VN; ++i) {
+                uint32_t w[4][VP / 4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    load_words<VP>(w[y],
+                                   stage + KT * RB + (((x * 4 + y) * VN + i) * 32 + lane) * VP);
+#pragma unroll
+                for (int z = 0; z < VP / 4; ++z) {
+                    uint32_t b0[4], b1[4];
+                    constexpr int E = k8 ? 4 : 2;
+                    if constexpr (k8) {
+                        const uint32_t u0 = __byte_perm(w[0][z], w[1][z], 0x5140);
+                        const uint32_t u1 = __byte_perm(w[0][z], w[1][z], 0x7362);
+                        const uint32_t u2 = __byte_perm(w[2][z], w[3][z], 0x5140);
+                        const uint32_t u3 = __byte_perm(w[2][z], w[3][z], 0x7362);
+                        b0[0] = widen(u0 & 0xffffu), b0[1] = widen(u0 >> 16);
+                        b0[2] = widen(u1 & 0xffffu), b0[3] = widen(u1 >> 16);
+                        b1[0] = widen(u2 & 0xffffu), b1[1] = widen(u2 >> 16);
+                        b1[2] = widen(u3 & 0xffffu), b1[3] = widen(u3 >> 16);
+                    } else {
+                        b0[0] = __byte_perm(w[0][z], w[1][z], 0x5410);
+                        b0[1] = __byte_perm(w[0][z], w[1][z], 0x7632);
+                        b1[0] = __byte_perm(w[2][z], w[3][z], 0x5410);
+                        b1[1] = __byte_perm(w[2][z], w[3][z], 0x7632);
+                    }
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+#pragma unroll
+                        for (int b = 0; b < NB; ++b) {
+                            const uint32_t pa[4] = {ph[b][2 * x], pl[b][2 * x], ph[b][2 * x + 1],
+                                                    pl[b][2 * x + 1]};
+                            mma(acc[b][i * VE + z * E + e], pa, b0[e], b1[e], T());
+                        }
+                }
+            }
+    }
+
+    // f(query, first column, four columns, m, l): the lane's share of the row.
+    template <typename F>
+    __device__ __forceinline__ void finish(F f) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            l[b] += __shfl_xor_sync(kFull, l[b], 1);
+            l[b] += __shfl_xor_sync(kFull, l[b], 2);
+            // (no weight at all: the sums are zero)
+            const float back = !k8 ? 1.f : mw[b] == -INFINITY ? 0.f : ex2(mw[b] - 14.f - m[b]);
+#pragma unroll
+            for (int i = 0; i < VN; ++i)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int e = 0; e < VE; e += 4) {
+                        float o[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const float hi = acc[b][i * VE + e + y][c];
+                            const float lo = acc[b][i * VE + e + y][2 + c];
+                            // (an infinite value times a remainder of zero)
+                            o[y] = (fabsf(hi) < INFINITY ? hi + lo : hi) * back;
+                        }
+                        f(b * 8 + g, (i * 8 + 2 * t + c) * VE + e,
+                          make_float4(o[0], o[1], o[2], o[3]), m[b], l[b]);
+                    }
+        }
+    }
+};
+
+// ------------------------------------------------------------ fp32 tiles
+
+template <int kD, int NB>
+struct FmaTile {
+    using Out = float;
+    static constexpr int D = kD, NQ = 8 * NB, RB = 4 * D, KT = 16;
+    static constexpr int kStages = D == 32 || NB == 2 ? 2 : 3, kWarps = D == 128 ? 4 : 8;
+    static constexpr int kOcc = D == 32 && NB == 1 ? 2 : 1;
+    static constexpr int kStageBytes = 2 * KT * RB;
+    static constexpr int kOwnBytes = NQ * D * 4 + NQ * KT * 4;  // queries and probabilities
+    static constexpr int C = D / 4;       // 16-byte pieces of a row
+    static constexpr int KG = 32 / C;     // keys side by side in the value sum
+    static constexpr int KE = KT / KG;    // keys of a lane
+
+    int lane, gq;
+    float *qs, *ps;
+    float m[NQ], l[NQ];
+    float4 acc[NQ];
+
+    __device__ __forceinline__ void begin(const DecodeArgs &a, void *own, int64_t n, int64_t h0,
+                                          int queries) {
+        lane = threadIdx.x & 31, gq = queries;
+        qs = (float *)own;
+        ps = qs + NQ * D;
+        __syncwarp();
+        for (int x = lane; x < gq * C; x += 32) {
+            float4 q = reinterpret_cast<const float4 *>((const float *)a.q + (n * a.H + h0) * D)[x];
+            q.x *= a.scale2, q.y *= a.scale2, q.z *= a.scale2, q.w *= a.scale2;
+            reinterpret_cast<float4 *>(qs)[x] = q;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+            m[x] = -INFINITY, l[x] = 0.f;
+            acc[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+    }
+
+    // Piece c of row r lies at place c ^ (r mod 8): eight lanes on eight rows
+    // meet eight banks.
+    __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage,
+                                         const int64_t *rows) const {
+        const uint32_t dst = smem_addr(stage);
+        const int ln = threadIdx.x & 31;
+#pragma unroll
+        for (int x = 0; x < KT * C; x += 32) {
+            const int at = x + ln, key = at / C, c = at % C;
+            const int64_t r = rows[key];
+            const int64_t src = (r < 0 ? 0 : r) * RB + c * 16;
+            const uint32_t to = dst + key * RB + ((c ^ (key & 7)) << 4);
+            copy_async<16>(to, (const uint8_t *)a.k + src, r >= 0);
+            copy_async<16>(to + KT * RB, (const uint8_t *)a.v + src, r >= 0);
+        }
+    }
+
+    __device__ __forceinline__ void tile(const uint8_t *stage, uint32_t mask) {
+        const int key = lane & 15, part = lane >> 4;
+        float s[NQ];
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) s[x] = 0.f;
+#pragma unroll 4
+        for (int c0 = 0; c0 < C / 2; ++c0) {
+            const int c = part * (C / 2) + c0;
+            const float4 k =
+                *reinterpret_cast<const float4 *>(stage + key * RB + ((c ^ (key & 7)) << 4));
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                if (x < gq) {
+                    const float4 q = reinterpret_cast<const float4 *>(qs)[x * C + c];
+                    s[x] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[x]))));
+                }
+        }
+        const bool on = (mask >> key) & 1;
+#pragma unroll
+        for (int x = 0; x < NQ; ++x)
+            if (x < gq) {
+                float z = s[x] + __shfl_xor_sync(kFull, s[x], 16);
+                if (!on) z = -INFINITY;
+                float top = z;
+#pragma unroll
+                for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                top = fmaxf(top, m[x]);
+                const float base = finite_base(top), fall = ex2(m[x] - base);
+                const float p = ex2(z - base);
+                m[x] = top;
+                l[x] = l[x] * fall + p;
+                acc[x].x *= fall, acc[x].y *= fall, acc[x].z *= fall, acc[x].w *= fall;
+                if (part == 0) ps[x * KT + key] = p;
+            }
+        __syncwarp();
+        const int c = lane % C, kg = lane / C;
+#pragma unroll
+        for (int k0 = 0; k0 < KE; k0 += 4) {
+            float4 v[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                const int j = kg * KE + k0 + y;
+                v[y] = *reinterpret_cast<const float4 *>(stage + KT * RB + j * RB +
+                                                         ((c ^ (j & 7)) << 4));
+            }
+#pragma unroll
+            for (int x = 0; x < NQ; ++x)
+                if (x < gq) {
+                    const float4 p =
+                        *reinterpret_cast<const float4 *>(ps + x * KT + kg * KE + k0);
+                    const float pp[4] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) {
+                        acc[x].x = fmaf(pp[y], v[y].x, acc[x].x);
+                        acc[x].y = fmaf(pp[y], v[y].y, acc[x].y);
+                        acc[x].z = fmaf(pp[y], v[y].z, acc[x].z);
+                        acc[x].w = fmaf(pp[y], v[y].w, acc[x].w);
+                    }
+                }
+        }
+        __syncwarp();
+    }
+
+    template <typename F>
+    __device__ __forceinline__ void finish(F f) {
+#pragma unroll
+        for (int x = 0; x < NQ; ++x) {
+#pragma unroll
+            for (int o = 8; o; o >>= 1) l[x] += __shfl_xor_sync(kFull, l[x], o);
+#pragma unroll
+            for (int o = C; o < 32; o <<= 1) {
+                acc[x].x += __shfl_xor_sync(kFull, acc[x].x, o);
+                acc[x].y += __shfl_xor_sync(kFull, acc[x].y, o);
+                acc[x].z += __shfl_xor_sync(kFull, acc[x].z, o);
+                acc[x].w += __shfl_xor_sync(kFull, acc[x].w, o);
+            }
+            if (lane < C) f(x, 4 * lane, acc[x], m[x], l[x]);
+        }
+    }
+};
+
+// ------------------------------------------------------------- the kernels
+
+template <typename Tile>
+struct Layout {
+    // per warp: the ring, the rows of the tile being copied, the stages' masks
+    static constexpr int kRing = Tile::kStages * Tile::kStageBytes;
+    static constexpr int kRows = kRing + Tile::kOwnBytes;
+    static constexpr int kMask = kRows + Tile::KT * 8;
+    static constexpr int kBytes = (kMask + Tile::kStages * 4 + 127) / 128 * 128;
+    using P = Part<Tile::NQ, Tile::D>;
+    // (a warp's partial row of the direct way lies where its ring was)
+    static_assert(P::kFloats * 4 <= kBytes, "a partial row fits a warp's storage");
+    static_assert(kBytes * Tile::kWarps * Tile::kOcc <= 227 * 1024 - 4096 * Tile::kOcc, "smem");
+};
+
+// Edges [x0, x1) of a token's row for one block of query heads.
+template <typename Tile>
+__device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const GraphView &g,
+                                          const Token &t, int64_t kvh, int32_t x0, int32_t x1,
+                                          uint8_t *mem) {
+    using M = Layout<Tile>;
+    constexpr int S = Tile::kStages, KT = Tile::KT;
+    const int lane = threadIdx.x & 31;
+    int64_t *rows = reinterpret_cast<int64_t *>(mem + M::kRows);
+    uint32_t *masks = reinterpret_cast<uint32_t *>(mem + M::kMask);
+    const int32_t n = (x1 - x0 + KT - 1) / KT;
+
+    int32_t at = x0 + lane;      // the next edge of this lane to look up
+    int32_t key = -1;            // its position
+    int32_t page = -1, off = -1; // page and place of the one before
+    auto next_key = [&] {
+        key = lane < KT && at < x1 ? (int32_t)row_edge(g, t.e, t.p, at) : -1;
+        at += KT;
+    };
+    auto next_page = [&] {
+        page = off = -1;
+        if (key >= 0) {
+            const uint32_t x = divide((uint32_t)key, a.page);
+            off = key - (int32_t)(x * a.page.by);
+            page = t.pages[x];
+        }
+    };
+    auto copy = [&](int stage) {
+        const bool ok = off >= 0 && page >= 0 && page < a.n_pages;
+        if (off >= 0 && !ok) atomicOr(a.err, SA_DEVERR_BOUNDS);
+        const uint32_t mask = __ballot_sync(kFull, ok);
+        __syncwarp();
+        if (lane < KT) rows[lane] = ok ? ((int64_t)page * a.Hkv + kvh) * a.page.by + off : -1;
+        if (lane == 0) masks[stage] = mask;
+        __syncwarp();
+        tile.copy(a, mem + stage * Tile::kStageBytes, rows);
+    };
+    next_key();
+    next_page();
+    next_key();
+    int stage = 0;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (i < n) {
+            copy(i);
+            next_page();
+            next_key();
+        }
+        copies_commit();
+    }
+    int ahead = S - 1;
+    for (int32_t i = 0; i < n; ++i) {
+        copies_wait<S - 2>();
+        __syncwarp();
+        if (i + S - 1 < n) {
+            copy(ahead);
+            next_page();
+            next_key();
+        }
+        copies_commit();
+        tile.tile(mem + stage * Tile::kStageBytes, masks[stage]);
+        stage = stage + 1 == S ? 0 : stage + 1;
+        ahead = ahead + 1 == S ? 0 : ahead + 1;
+    }
+    copies_wait<0>();
+    __syncwarp();
+}
+
+template <typename Tile>
+__device__ __forceinline__ void write_part(Tile &tile, float *slot) {
+    constexpr int NQ = Tile::NQ, D = Tile::D;
+    tile.finish([&](int q, int d, float4 o, float m, float l) {
+        *reinterpret_cast<float4 *>(slot + 2 * NQ + q * D + d) = o;
+        if (d == 0) slot[q] = m, slot[NQ + q] = l;
+    });
+}
+
+template <typename Tile>
+__device__ __forceinline__ void write_out(Tile &tile, const DecodeArgs &a, int64_t nh, int gq) {
+    using Out = typename Tile::Out;
+    tile.finish([&](int q, int d, float4 o, float m, float l) {
+        if (q >= gq) return;
+        State s;
+        s.m = m, s.l = l;
+        store4((Out *)a.out + (nh + q) * Tile::D + d, divided(o, l));
+        if (d == 0) a.lse[nh + q] = s.lse();
+    });
+}
+
+// Merge of partial rows by the whole CTA; slot(i) is the i-th of `count`.
+template <typename Tile, typename Slot>
+__device__ __forceinline__ void merge_parts(const DecodeArgs &a, Slot slot, int count, float *to,
+                                            int64_t nh, int gq) {
+    constexpr int NQ = Tile::NQ, D = Tile::D, C = D / 4;
+    for (int x = threadIdx.x; x < gq * C; x += blockDim.x) {
+        const int q = x / C, d = x % C * 4;
+        State s;
+        for (int i = 0; i < count; ++i) {
+            const float *p = slot(i);
+            s.add(p[q], p[NQ + q], *reinterpret_cast<const float4 *>(p + 2 * NQ + q * D + d));
+        }
+        if (to) {
+            *reinterpret_cast<float4 *>(to + 2 * NQ + q * D + d) = s.o;
+            if (d == 0) to[q] = s.m, to[NQ + q] = s.l;
+        } else {
+            store4((typename Tile::Out *)a.out + (nh + q) * D + d, divided(s.o, s.l));
+            if (d == 0) a.lse[nh + q] = s.lse();
+        }
     }
 }
 
-template <typename T, int D>
-sa_status launch_decode(const DecodeArgs &a, const GraphView &g, int64_t blocks, cudaStream_t s) {
-    if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
+// Query heads of block u of a token: first head and how many.
+struct Block {
+    int64_t kvh;
+    int32_t first, gq;
+};
+template <int NQ>
+__device__ __forceinline__ Block block_of(const DecodeArgs &a, int32_t u) {
+    const int32_t kvh = u / a.QB, q0 = (u - kvh * a.QB) * NQ;
+    return {kvh, kvh * a.G + q0, min(NQ, a.G - q0)};
+}
+
+// The direct way: CTA b has block b mod U of token b / U.
+template <typename Tile>
+__global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
+    paged_decode_direct(DecodeArgs a, GraphView g) {
+    using M = Layout<Tile>;
+    extern __shared__ __align__(128) uint8_t mem[];
+    const int U = a.Hkv * a.QB, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
+    const int64_t n = blockIdx.x / U;
+    const Block b = block_of<Tile::NQ>(a, blockIdx.x % U);
+    const Token t = token_of(a, g, n);
+    if (t.bad && threadIdx.x == 0) atomicOr(a.err, SA_DEVERR_BOUNDS);
+    const int32_t tiles = (t.deg + Tile::KT - 1) / Tile::KT;
+    const int32_t x0 = (int32_t)((int64_t)tiles * warp / nw) * Tile::KT;
+    const int32_t x1 = min(t.deg, (int32_t)((int64_t)tiles * (warp + 1) / nw) * Tile::KT);
+    uint8_t *own = mem + warp * M::kBytes;
+    Tile tile;
+    tile.begin(a, own + M::kRing, n, b.first, b.gq);
+    run_edges(tile, a, g, t, b.kvh, x0, x1, own);
+    if (nw == 1) {
+        write_out(tile, a, n * a.H + b.first, b.gq);
+        return;
+    }
+    write_part(tile, (float *)own);
+    __syncthreads();
+    merge_parts<Tile>(
+        a, [&](int i) { return (const float *)(mem + i * M::kBytes); }, nw, nullptr,
+        n * a.H + b.first, b.gq);
+}
+
+// Equal shares of `total` tiles.
+struct Shares {
+    int64_t base, rem;
+    __device__ Shares(int64_t total, int64_t n) : base(total / n), rem(total % n) {}
+    __device__ int64_t begin(int64_t w) const { return w * base + (w < rem ? w : rem); }
+    __device__ int64_t of(int64_t x) const {
+        const int64_t big = rem * (base + 1);
+        return x < big ? x / (base + 1) : rem + (x - big) / base;
+    }
+};
+
+// Fewest tiles worth a warp: below, a share is mostly its own start and merge.
+constexpr int kLeastTiles = 4;
+
+template <typename Tile>
+__global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
+    paged_decode_split(DecodeArgs a, GraphView g) {
+    using M = Layout<Tile>;
+    constexpr int NW = Tile::kWarps, NT = 32 * NW, KT = Tile::KT;
+    constexpr int PF = M::P::kFloats;
+    extern __shared__ __align__(128) uint8_t mem[];
+    __shared__ int64_t s_start[NT + 1];  // row tiles before each thread's rows
+    __shared__ int64_t s_sum[NW];
+    __shared__ int64_t s_unit[NW][2];    // the cut rows of each warp: one it goes on with, one
+    __shared__ int64_t s_end[NW];        //   it starts; the end of the latter
+    __shared__ int s_ends[NW];           // the former ends here
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t U = (int64_t)a.Hkv * a.QB;
+    auto tiles_of = [&](int32_t deg) { return max(1, (deg + KT - 1) / KT); };
+
+    // how many tiles there are, and where each run of rows begins
+    const int64_t per = (a.N + NT - 1) / NT;
+    {
+        int64_t own = 0;
+        for (int64_t n = tid * per; n < min(a.N, (tid + 1) * per); ++n)
+            own += tiles_of(token_of(a, g, n).deg);
+        int64_t x = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t y = __shfl_up_sync(kFull, x, o);
+            if (lane >= o) x += y;
+        }
+        if (lane == 31) s_sum[warp] = x;
+        if (lane < 2) s_unit[warp][lane] = -1;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) x += s_sum[w];
+        s_start[tid + 1] = x;
+        if (tid == 0) s_start[0] = 0;
+        __syncthreads();
+    }
+    const int64_t total = s_start[NT] * U;
+    const int64_t want = (total + (int64_t)kLeastTiles * gridDim.x - 1) /
+                         ((int64_t)kLeastTiles * gridDim.x);
+    const int nw = want < NW ? (int)want : NW;  // warps at work in each CTA
+    const Shares shares(total, (int64_t)nw * gridDim.x);
+    const int64_t W = (int64_t)blockIdx.x * nw + warp;
+    int64_t x = warp < nw ? shares.begin(W) : 0;
+    const int64_t x_end = warp < nw ? shares.begin(W + 1) : 0;
+    uint8_t *own = mem + warp * M::kBytes;
+    if (x < x_end) {
+        // the row of tile x
+        const int64_t y = x / U;
+        int lo = 0, hi = NT - 1;  // last run that begins at or before y
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (s_start[mid] <= y) lo = mid;
+            else hi = mid - 1;
+        }
+        int64_t n = lo * per, before = s_start[lo];
+        if (per > 1) {
+            for (;; n += 32) {
+                const int64_t mine = n + lane;
+                int64_t z = mine < a.N ? tiles_of(token_of(a, g, mine).deg) : 0;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t up = __shfl_up_sync(kFull, z, o);
+                    if (lane >= o) z += up;
+                }
+                const unsigned past = __ballot_sync(kFull, before + z > y);
+                if (past || n + 32 >= a.N) {
+                    const int f = past ? __ffs(past) - 1 : 31;
+                    const int64_t b4 = __shfl_sync(kFull, z, f ? f - 1 : 0);
+                    if (f) before += b4;
+                    n += f;
+                    break;
+                }
+                before += __shfl_sync(kFull, z, 31);
+            }
+        }
+        n = min(n, a.N - 1);
+        Token t = token_of(a, g, n);
+        int64_t in_row = x - before * U;
+        int32_t tiles = tiles_of(t.deg);
+        int32_t u = (int32_t)(in_row / tiles);
+        int32_t tile0 = (int32_t)(in_row - (int64_t)u * tiles);
+        Tile tile;
+        while (true) {
+            if (t.bad && lane == 0) atomicOr(a.err, SA_DEVERR_BOUNDS);
+            const int32_t run = (int32_t)min((int64_t)(tiles - tile0), x_end - x);
+            const Block b = block_of<Tile::NQ>(a, u);
+            tile.begin(a, own + M::kRing, n, b.first, b.gq);
+            run_edges(tile, a, g, t, b.kvh, tile0 * KT, min(t.deg, (tile0 + run) * KT), own);
+            const bool goes_on = tile0 > 0, ends = tile0 + run == tiles;
+            if (!goes_on && ends) {
+                write_out(tile, a, n * a.H + b.first, b.gq);
+            } else {
+                const int which = goes_on ? 0 : 1;
+                write_part(tile, a.warp_part + (W * 2 + which) * PF);
+                if (lane == 0) {
+                    s_unit[warp][which] = n * U + u;
+                    if (goes_on) s_ends[warp] = ends;
+                    else s_end[warp] = x + tiles;
+                }
+            }
+            x += run;
+            if (x >= x_end) break;
+            tile0 = 0;
+            if (++u == U) {
+                u = 0;
+                t = token_of(a, g, ++n);
+                tiles = tiles_of(t.deg);
+            }
+        }
+    }
+    __syncthreads();
+
+    // the CTA's cut rows, in order: each is merged over its warps
+    int4 cut = make_int4(-1, -1, 0, 0);
+    for (int i = 0; i < 2 * NW;) {
+        const int64_t unit = s_unit[i >> 1][i & 1];
+        if (unit < 0) {
+            ++i;
+            continue;
+        }
+        const bool starts = i & 1;
+        const int first = i;
+        int count = 0, last = i;
+        // (entries of other rows, or none, lie between a row's parts only where
+        // they are empty)
+        for (; i < 2 * NW; ++i) {
+            const int64_t other = s_unit[i >> 1][i & 1];
+            if (other == unit) last = i, ++count;
+            else if (other >= 0) break;
+        }
+        const bool ends = !(last & 1) && s_ends[last >> 1];
+        const int64_t n = unit / U;
+        const Block b = block_of<Tile::NQ>(a, (int32_t)(unit - n * U));
+        float *to = starts && ends ? nullptr
+                                   : a.cta_part + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * PF;
+        // parts of one row: slot 1 of the warp it starts in, then slots 0
+        const int w0 = first >> 1;
+        merge_parts<Tile>(
+            a,
+            [&](int k) {
+                const int slot = starts && k == 0 ? 1 : 0;
+                return (const float *)a.warp_part +
+                       (((int64_t)blockIdx.x * nw + w0 + k) * 2 + slot) * PF;
+            },
+            count, to, n * a.H + b.first, b.gq);
+        if (starts && !ends)
+            cut = make_int4((int)(unit & 0xffffffff), (int)(unit >> 32),
+                            (int)(shares.of(s_end[first >> 1] - 1) / nw), 0);
+    }
+    if (tid == 0) a.cut[blockIdx.x] = cut;
+}
+
+// The rows cut between CTAs: block (c, q) joins query q of the row that starts
+// in CTA c and goes on.
+constexpr int kJoinThreads = 256;
+
+template <typename Tile>
+__global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) {
+    constexpr int NQ = Tile::NQ, D = Tile::D, C = D / 4, R = kJoinThreads / C;
+    constexpr int PF = Part<NQ, D>::kFloats;
+    __shared__ float s_m[R], s_l[R];
+    __shared__ float4 s_o[R][C];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int4 cut = __ldcg(a.cut + blockIdx.x);
+    const int64_t unit = (int64_t)(uint32_t)cut.x | ((int64_t)cut.y << 32);
+    if (unit < 0) return;
+    const int64_t U = (int64_t)a.Hkv * a.QB, n = unit / U;
+    const Block b = block_of<NQ>(a, (int32_t)(unit - n * U));
+    const int q = blockIdx.y, c = threadIdx.x % C, r = threadIdx.x / C;
+    if (q >= b.gq) return;
+    const int count = cut.z - (int)blockIdx.x + 1;
+    State s;
+#pragma unroll 4
+    for (int i = r; i < count; i += R) {
+        const float *p = a.cta_part + (((int64_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * PF;
+        s.add(__ldcg(p + q), __ldcg(p + NQ + q),
+              __ldcg(reinterpret_cast<const float4 *>(p + 2 * NQ + q * D + 4 * c)));
+    }
+    if (c == 0) s_m[r] = s.m, s_l[r] = s.l;
+    s_o[r][c] = s.o;
+    __syncthreads();
+    if (r != 0) return;
+#pragma unroll
+    for (int i = 1; i < R; ++i) s.add(s_m[i], s_l[i], s_o[i][c]);
+    const int64_t nh = n * a.H + b.first + q;
+    store4((typename Tile::Out *)a.out + nh * D + 4 * c, divided(s.o, s.l));
+    if (c == 0) a.lse[nh] = s.lse();
+}
+
+// ------------------------------------------------------------------- host
+
+// Longest row that the direct way takes.
+constexpr int64_t kDirectKeys = 512;
+
+int64_t longest_row(const sa_graph_s *g) {
+    int64_t n = g->kind == 0 ? (int64_t)g->W + g->n_off
+                             : (int64_t)g->W + g->max_resid;
+    return n < g->T ? n : g->T;
+}
+
+// f(a Tile type) for this cache and group size.
+template <typename F>
+auto with_tile(const sa_paged_cache &c, int64_t G, F f)
+    -> decltype(f((MmaTile<E4m3, 32, 1> *)0)) {
+#define SA_PAGED_TILE(d)                                                              \
+    if (c.D == d) {                                                                   \
+        if (c.dtype == SA_BF16)                                                       \
+            return G > 8 ? f((MmaTile<__nv_bfloat16, d, 2> *)0)                       \
+                         : f((MmaTile<__nv_bfloat16, d, 1> *)0);                      \
+        if (c.dtype == SA_E4M3)                                                       \
+            return G > 8 ? f((MmaTile<E4m3, d, 2> *)0) : f((MmaTile<E4m3, d, 1> *)0); \
+        return G > 8 ? f((FmaTile<d, 2> *)0) : f((FmaTile<d, 1> *)0);                 \
+    }
+    SA_PAGED_TILE(32)
+    SA_PAGED_TILE(64)
+    SA_PAGED_TILE(128)
+#undef SA_PAGED_TILE
+    return {};
+}
+
+struct Plan {
+    int64_t ctas = 0, part_floats = 0, warps = 0;
+    size_t bytes() const {
+        return ctas ? (size_t)(ctas * (warps + 1) * 2 * part_floats * 4 + ctas * 16) : 0;
+    }
+};
+
+template <typename Tile>
+Plan split_plan(int sms) {
+    Plan p;
+    p.ctas = (int64_t)sms * Tile::kOcc;
+    p.part_floats = Part<Tile::NQ, Tile::D>::kFloats;
+    p.warps = Tile::kWarps;
+    return p;
+}
+
+template <typename Tile>
+sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, void *workspace,
+                        cudaStream_t s) {
+    using M = Layout<Tile>;
+    a.QB = (a.G + Tile::NQ - 1) / Tile::NQ;
+    if (longest <= kDirectKeys) {
+        const int64_t blocks = a.N * a.Hkv * a.QB;
+        if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
+        int nw = (int)((longest + Tile::KT - 1) / Tile::KT);
+        nw = nw < 1 ? 1 : nw > Tile::kWarps ? Tile::kWarps : nw;
+        SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_direct<Tile>,
+                                  Tile::kWarps * M::kBytes));
+        SA_LAUNCH("paged_decode", s,
+                  paged_decode_direct<Tile>
+                  <<<(unsigned)blocks, 32 * nw, nw * M::kBytes, s>>>(a, g));
+        SA_CUDA_TRY(cudaGetLastError());
+        return SA_OK;
+    }
+    int sms = 0;
+    SA_CUDA_TRY(sa_sm_count(&sms));
+    const Plan p = split_plan<Tile>(sms);
+    a.warp_part = (float *)workspace;
+    a.cta_part = a.warp_part + p.ctas * p.warps * 2 * p.part_floats;
+    a.cut = (int4 *)(a.cta_part + p.ctas * 2 * p.part_floats);
+    SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_split<Tile>, Tile::kWarps * M::kBytes));
     SA_LAUNCH("paged_decode", s,
-              paged_decode_kernel<T, D><<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, g));
+              paged_decode_split<Tile>
+              <<<(unsigned)p.ctas, 32 * Tile::kWarps, Tile::kWarps * M::kBytes, s>>>(a, g));
     SA_CUDA_TRY(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(a.G < Tile::NQ ? a.G : Tile::NQ));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = s;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaSuccess;
+    SA_LAUNCH("paged_decode_join", s, e = cudaLaunchKernelEx(&cfg, paged_decode_join<Tile>, a));
+    SA_CUDA_TRY(e);
     return SA_OK;
 }
 
 }  // namespace
 
-size_t sa_paged_decode_workspace(const sa_tensor *, const sa_paged_cache &, const sa_graph_s *) {
-    return 0;
+size_t sa_paged_decode_workspace(const sa_tensor *q, const sa_paged_cache &c,
+                                 const sa_graph_s *g) {
+    int sms = 0;
+    if (longest_row(g) <= kDirectKeys || sa_sm_count(&sms) != cudaSuccess) return 0;
+    return with_tile(c, q->H / c.Hkv, [&](auto *t) {
+        return split_plan<std::remove_pointer_t<decltype(t)>>(sms);
+    }).bytes();
 }
 
 sa_status sa_paged_decode(const sa_tensor *q, const sa_paged_cache &c, const int32_t *table,
                           int64_t rows, int64_t max_pages, const int32_t *row, const int64_t *pos,
                           const sa_graph_s *g, float scale, sa_tensor *out, float *lse,
                           void *workspace, cudaStream_t s) {
-    (void)workspace;
     DecodeArgs a = {};
     a.q = q->ptr;
     a.k = c.k;
@@ -188,31 +1125,25 @@ sa_status sa_paged_decode(const sa_tensor *q, const sa_paged_cache &c, const int
     a.table = table;
     a.row = row;
     a.pos = pos;
+    a.N = q->B;
     a.rows = rows;
     a.max_pages = max_pages;
     a.n_pages = c.n_pages;
     a.H = (int32_t)q->H;
     a.Hkv = (int32_t)c.Hkv;
-    a.P = (int32_t)c.page_size;
+    a.G = (int32_t)(q->H / c.Hkv);
+    a.page = make_divide((uint32_t)c.page_size);
     a.scale2 = scale * kLog2e;
     a.out = out->ptr;
     a.lse = lse;
     a.err = sa_device_error_word();
     if (!a.err) return SA_ERR_CUDA;
     const GraphView gv = make_view(g);
-    const int64_t blocks = q->B * q->H;
-#define SA_PAGED_DECODE(D)                                                            \
-    switch (c.dtype) {                                                                \
-        case SA_BF16: return launch_decode<__nv_bfloat16, D>(a, gv, blocks, s);       \
-        case SA_FP32: return launch_decode<float, D>(a, gv, blocks, s);               \
-        case SA_E4M3: return launch_decode<E4m3, D>(a, gv, blocks, s);                \
-    }                                                                                 \
-    break;
-    switch (c.D) {
-        case 32: SA_PAGED_DECODE(32)
-        case 64: SA_PAGED_DECODE(64)
-        case 128: SA_PAGED_DECODE(128)
-    }
-#undef SA_PAGED_DECODE
-    return SA_ERR_UNSUPPORTED;
+    struct Result {
+        sa_status st = SA_ERR_UNSUPPORTED;
+    };
+    return with_tile(c, a.G, [&](auto *t) {
+        return Result{launch_decode<std::remove_pointer_t<decltype(t)>>(a, gv, longest_row(g),
+                                                                       workspace, s)};
+    }).st;
 }
