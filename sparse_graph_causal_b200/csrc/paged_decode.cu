@@ -18,9 +18,8 @@
 // time that the bytes take, so the shape wastes nothing that counts, and the
 // warp needs no other warp.  The sums over d (of S) and the columns (of O) may
 // be taken in any order, so a lane's fragment is whatever 16 bytes of a row it
-// can load at once: each lane copies the very bytes that it multiplies, and
-// the stages are its own storage, without bank conflicts or a layout.
-//   S: lane (g, t) = (lane / 4, lane % 4) holds 16-byte pieces t, t + 4, ... of
+// can load at once:
+//   S: lane (g, t) = (lane / 4, lane % 4) multiplies 16-byte pieces t, t + 4, ... of
 //      key g;  O: pieces g, g + 8, ... of the value rows 2t, 2t+1, 2t+8, 2t+9.
 // P has 16 bits in the product; with one 8-head block the lower eight rows of
 // the tile are free and carry what the rounding of P left over (P = hi + lo, 2^-17),
@@ -319,36 +318,45 @@ struct MmaTile {
         }
     }
 
-    // Start the copies of a tile: rows[] are the cache rows of its keys, -1 for none.
+    // Where 16-byte piece c of row r lies in a staged tile: rows one after the
+    // other, the eight pieces of each 128 bytes permuted so that the lanes that
+    // read together meet different banks (keys: two neighbouring rows, values:
+    // four rows two apart).
+    __device__ __forceinline__ static uint32_t place(int r, int c, int f) {
+        const uint32_t at = r * RB + c * 16;
+        return at ^ (uint32_t)(f << 4);
+    }
+    __device__ __forceinline__ static uint32_t key_place(int r, int c) {
+        return place(r, c, RB >= 128 ? (r & 1) << 2 : 0);
+    }
+    __device__ __forceinline__ static uint32_t value_place(int r, int c) {
+        return place(r, c, RB >= 64 ? ((r >> 1) & 3) << 1 : 0);
+    }
+
+    // Start the copies of a tile: at[] are the offsets of its rows in the
+    // cache, in bytes, -1 for none.  A row's lanes are neighbours.
     __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage,
-                                         const int64_t *rows) const {
-        const uint32_t dst = smem_addr(stage) + (threadIdx.x & 31) * KP;
-        const int ln = threadIdx.x & 31, gg = ln >> 2, tt = ln & 3;
+                                         const int64_t *at) const {
+        constexpr int L = RB / 16, R = 32 / L;
+        const int ln = threadIdx.x & 31, sub = ln % L, h = ln / L;
+        const uint32_t dst = smem_addr(stage);
 #pragma unroll
-        for (int x = 0; x < KT / 8; ++x) {
-            const int64_t r = rows[x * 8 + gg];
-            const uint8_t *src = (const uint8_t *)a.k + (r < 0 ? 0 : r) * RB + tt * KP;
-#pragma unroll
-            for (int i = 0; i < KN; ++i)
-                copy_async<KP>(dst + (x * KN + i) * 32 * KP, src + i * 4 * KP, r >= 0);
-        }
-        const uint32_t vdst = smem_addr(stage) + KT * RB + ln * VP;
-#pragma unroll
-        for (int x = 0; x < KT / 4; ++x) {
-            const int64_t r = rows[x / 4 * 16 + (x & 2) * 4 + 2 * tt + (x & 1)];
-            const uint8_t *src = (const uint8_t *)a.v + (r < 0 ? 0 : r) * RB + gg * VP;
-#pragma unroll
-            for (int i = 0; i < VN; ++i)
-                copy_async<VP>(vdst + (x * VN + i) * 32 * VP, src + i * 8 * VP, r >= 0);
+        for (int x = 0; x < KT / R; ++x) {
+            const int64_t o = at[x * R + h];
+            const bool on = o >= 0;
+            const int64_t src = (on ? o : 0) + sub * 16;
+            copy_async<16>(dst + key_place(x * R + h, sub), (const uint8_t *)a.k + src, on);
+            copy_async<16>(dst + KT * RB + value_place(x * R + h, sub), (const uint8_t *)a.v + src,
+                           on);
         }
         if constexpr (k8) {
-            const uint32_t sdst = smem_addr(stage) + 2 * KT * RB;
+            const uint32_t sdst = dst + 2 * KT * RB;
 #pragma unroll
             for (int x = 0; x < 2 * KT; x += 32) {
-                const int at = x + ln, key = at % KT;
-                const int64_t r = rows[key];
-                copy_async<4>(sdst + 4 * at, (at < KT ? a.k_scale : a.v_scale) + (r < 0 ? 0 : r),
-                              r >= 0);
+                const int i = x + ln;
+                const int64_t o = at[i % KT];
+                copy_async<4>(sdst + 4 * i, (i < KT ? a.k_scale : a.v_scale) + (o < 0 ? 0 : o / RB),
+                              o >= 0);
             }
         }
     }
@@ -360,11 +368,13 @@ struct MmaTile {
         // scores
 #pragma unroll
         for (int x = 0; x < KB; ++x) {
-            s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+            float s2[2][4] = {};  // two sums side by side: half the chain
             uint32_t w[KN * KP / 4];
 #pragma unroll
-            for (int i = 0; i < KN; ++i)
-                load_words<KP>(w + i * KP / 4, stage + ((x * KN + i) * 32 + lane) * KP);
+            for (int i = 0; i < KN; ++i) {
+                const int c = (i * 4 + t) * KP;  // byte of the row
+                load_words<KP>(w + i * KP / 4, stage + key_place(x * 8 + g, c / 16) + c % 16);
+            }
 #pragma unroll
             for (int y = 0; y < KS; ++y) {
                 uint32_t qa[4];
@@ -373,11 +383,14 @@ struct MmaTile {
                 qa[1] = NB == 1 ? 0 : qf[y][NB - 1];
                 qa[3] = NB == 1 ? 0 : qf[y][2 * NB - 1];
                 if constexpr (k8)
-                    mma(s[x], qa, widen(w[y] & 0xffffu), widen(w[y] >> 16), T());
+                    mma(s2[y & 1], qa, widen(w[y] & 0xffffu), widen(w[y] >> 16), T());
                 else
-                    mma(s[x], qa, w[2 * y], w[2 * y + 1], T());
+                    mma(s2[y & 1], qa, w[2 * y], w[2 * y + 1], T());
             }
+#pragma unroll
+            for (int y = 0; y < 4; ++y) s[x][y] = s2[0][y] + s2[1][y];
         }
+        const uint32_t all = KT == 32 ? kFull : (1u << KT) - 1;
         uint32_t ph[NB][KB], pl[NB][KB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -390,12 +403,12 @@ struct MmaTile {
                     const int key = x * 8 + 2 * t + y;
                     float z = s[x][2 * b + y] * unit[b];
                     if constexpr (k8) z *= scales[key];
-                    if (!((mask >> key) & 1)) z = -INFINITY;
+                    if (mask != all && !((mask >> key) & 1)) z = -INFINITY;
                     s[x][2 * b + y] = z;
                     top = fmaxf(top, z);
                     if constexpr (k8) {
                         lv[x][y] = lg2(fabsf(scales[KT + key]));
-                        if (!((mask >> key) & 1)) lv[x][y] = 0.f;
+                        if (mask != all && !((mask >> key) & 1)) lv[x][y] = 0.f;
                         topw = fmaxf(topw, z + lv[x][y]);
                     }
                 }
@@ -440,9 +453,12 @@ struct MmaTile {
             for (int i = 0; i < VN; ++i) {
                 uint32_t w[4][VP / 4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y)
-                    load_words<VP>(w[y],
-                                   stage + KT * RB + (((x * 4 + y) * VN + i) * 32 + lane) * VP);
+                for (int y = 0; y < 4; ++y) {
+                    const int c = (i * 8 + g) * VP;
+                    load_words<VP>(w[y], stage + KT * RB + c % 16 +
+                                             value_place(x * 16 + (y & 2) * 4 + 2 * t + (y & 1),
+                                                         c / 16));
+                }
 #pragma unroll
                 for (int z = 0; z < VP / 4; ++z) {
                     uint32_t b0[4], b1[4];
@@ -545,17 +561,17 @@ struct FmaTile {
     // Piece c of row r lies at place c ^ (r mod 8): eight lanes on eight rows
     // meet eight banks.
     __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage,
-                                         const int64_t *rows) const {
+                                         const int64_t *at) const {
         const uint32_t dst = smem_addr(stage);
         const int ln = threadIdx.x & 31;
 #pragma unroll
         for (int x = 0; x < KT * C; x += 32) {
-            const int at = x + ln, key = at / C, c = at % C;
-            const int64_t r = rows[key];
-            const int64_t src = (r < 0 ? 0 : r) * RB + c * 16;
+            const int key = (x + ln) / C, c = (x + ln) % C;
+            const int64_t o = at[key];
+            const int64_t src = (o < 0 ? 0 : o) + c * 16;
             const uint32_t to = dst + key * RB + ((c ^ (key & 7)) << 4);
-            copy_async<16>(to, (const uint8_t *)a.k + src, r >= 0);
-            copy_async<16>(to + KT * RB, (const uint8_t *)a.v + src, r >= 0);
+            copy_async<16>(to, (const uint8_t *)a.k + src, o >= 0);
+            copy_async<16>(to + KT * RB, (const uint8_t *)a.v + src, o >= 0);
         }
     }
 
@@ -666,12 +682,17 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
     int64_t *rows = reinterpret_cast<int64_t *>(mem + M::kRows);
     uint32_t *masks = reinterpret_cast<uint32_t *>(mem + M::kMask);
     const int32_t n = (x1 - x0 + KT - 1) / KT;
+    const int32_t p = (int32_t)t.p, window = (int32_t)t.e.lo - t.e.ndil;
 
     int32_t at = x0 + lane;      // the next edge of this lane to look up
     int32_t key = -1;            // its position
     int32_t page = -1, off = -1; // page and place of the one before
     auto next_key = [&] {
-        key = lane < KT && at < x1 ? (int32_t)row_edge(g, t.e, t.p, at) : -1;
+        key = -1;
+        if (lane < KT && at < x1)
+            key = g.kind != 0        ? g.colidx[t.e.start + at]
+                  : at < t.e.ndil    ? p - (int32_t)g.offs[t.e.first + at]
+                                     : window + at;
         at += KT;
     };
     auto next_page = [&] {
@@ -687,7 +708,9 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
         if (off >= 0 && !ok) atomicOr(a.err, SA_DEVERR_BOUNDS);
         const uint32_t mask = __ballot_sync(kFull, ok);
         __syncwarp();
-        if (lane < KT) rows[lane] = ok ? ((int64_t)page * a.Hkv + kvh) * a.page.by + off : -1;
+        if (lane < KT)
+            rows[lane] =
+                ok ? (((int64_t)page * a.Hkv + kvh) * a.page.by + off) * Tile::RB : -1;
         if (lane == 0) masks[stage] = mask;
         __syncwarp();
         tile.copy(a, mem + stage * Tile::kStageBytes, rows);
@@ -697,7 +720,7 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
     next_key();
     int stage = 0;
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
+    for (int i = 0; i < S; ++i) {
         if (i < n) {
             copy(i);
             next_page();
@@ -705,19 +728,20 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
         }
         copies_commit();
     }
-    int ahead = S - 1;
+    // (the copies of a later tile come after the work on this one: in front they
+    // would hold up its loads from shared memory)
     for (int32_t i = 0; i < n; ++i) {
-        copies_wait<S - 2>();
+        copies_wait<S - 1>();
         __syncwarp();
-        if (i + S - 1 < n) {
-            copy(ahead);
+        tile.tile(mem + stage * Tile::kStageBytes, masks[stage]);
+        __syncwarp();
+        if (i + S < n) {
+            copy(stage);
             next_page();
             next_key();
         }
         copies_commit();
-        tile.tile(mem + stage * Tile::kStageBytes, masks[stage]);
         stage = stage + 1 == S ? 0 : stage + 1;
-        ahead = ahead + 1 == S ? 0 : ahead + 1;
     }
     copies_wait<0>();
     __syncwarp();
@@ -752,9 +776,19 @@ __device__ __forceinline__ void merge_parts(const DecodeArgs &a, Slot slot, int 
     for (int x = threadIdx.x; x < gq * C; x += blockDim.x) {
         const int q = x / C, d = x % C * 4;
         State s;
-        for (int i = 0; i < count; ++i) {
-            const float *p = slot(i);
-            s.add(p[q], p[NQ + q], *reinterpret_cast<const float4 *>(p + 2 * NQ + q * D + d));
+        constexpr int kAtOnce = 8;
+        for (int i0 = 0; i0 < count; i0 += kAtOnce) {
+            float m[kAtOnce], l[kAtOnce];
+            float4 o[kAtOnce];
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+                const float *p = slot(min(i0 + i, count - 1));
+                m[i] = p[q], l[i] = p[NQ + q];
+                o[i] = *reinterpret_cast<const float4 *>(p + 2 * NQ + q * D + d);
+            }
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i)
+                if (i0 + i < count) s.add(m[i], l[i], o[i]);
         }
         if (to) {
             *reinterpret_cast<float4 *>(to + 2 * NQ + q * D + d) = s.o;
