@@ -128,11 +128,13 @@ def _check(status: int, where: str):
 
 
 def _stream(stream):
-    if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    if stream is None:  # the current stream's handle, without making a Stream object
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     if isinstance(stream, torch.cuda.Stream):
-        return ctypes.c_void_p(stream.cuda_stream)
-    return ctypes.c_void_p(int(stream))
+        return stream.cuda_stream
+    return int(stream)
 
 
 def _tensor(t: torch.Tensor, name: str) -> SaTensor:
@@ -331,22 +333,25 @@ def sparse_attn_decode(q, k_cache, v_cache, pos, g: Graph, scale: float, out=Non
 _PAGED_DTYPES = {torch.bfloat16: SA_BF16, torch.float32: SA_FP32, torch.float8_e4m3fn: SA_E4M3}
 
 
-def _array(t, name: str, dtype, shape, device):
-    """Address of a contiguous tensor of this type and shape on this device."""
+def _array(t, name: str, dtype, shape, index: int) -> int:
+    """Address of a contiguous tensor of this type and shape on CUDA device `index`."""
     if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape \
-            or t.device != device or not t.is_contiguous():
+            or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} "
-                         f"on {device}")
+                         f"on cuda:{index}")
     return t.data_ptr()
 
 
-def _call_on(device, stream, call):
-    """call(stream) with the tensors' device current (the library launches on
-    the current one), on its current stream unless one is given."""
-    if device.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(device):
-        return call(_stream(stream))
+def _call_on(index: int, stream, where: str, fn, *args):
+    """fn(*args, stream) with the tensors' device current (the library launches
+    on the current one), on its current stream unless one is given."""
+    if index == torch._C._cuda_getDevice():
+        status = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _stream(stream))
+    if status != SA_OK:
+        _check(status, where)
 
 
 class PagedCache:
@@ -358,17 +363,26 @@ class PagedCache:
                 or k.dtype not in _PAGED_DTYPES:
             raise ValueError("k must be a CUDA [n_pages, Hkv, page_size, D] tensor in bf16, fp32 "
                              "or float8_e4m3fn")
-        kp, vp = (_array(x, n, k.dtype, k.shape, k.device) for x, n in ((k, "k"), (v, "v")))
+        index = k.get_device()
+        kp, vp = (_array(x, n, k.dtype, k.shape, index) for x, n in ((k, "k"), (v, "v")))
         ks = vs = None
         if k.dtype is torch.float8_e4m3fn:
-            ks, vs = (_array(x, n, torch.float32, k.shape[:3], k.device)
+            ks, vs = (_array(x, n, torch.float32, k.shape[:3], index)
                       for x, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
         elif k_scale is not None or v_scale is not None:
             raise ValueError("only float8_e4m3fn pages have scales")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.device, self.page_size = k.device, k.shape[2]
-        n, h, p, d = k.shape
-        self._desc = SaPagedCache(kp, vp, ks, vs, _PAGED_DTYPES[k.dtype], n, h, p, d)
+        self._tensors = k, v, k_scale, v_scale
+        n, self._heads, self._page, self._dim = k.shape
+        self._desc = SaPagedCache(kp, vp, ks, vs, _PAGED_DTYPES[k.dtype], n, self._heads,
+                                  self._page, self._dim)
+        self._index, self._ref = index, ctypes.byref(self._desc)
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
+    page_size = property(lambda self: self._page)
+    device = property(lambda self: self._tensors[0].device)
 
 
 class PagedBatch:
@@ -377,11 +391,21 @@ class PagedBatch:
     int32 [B] (SA_PAGED_OK, SA_PAGED_NO_PAGES or SA_PAGED_REFUSED)."""
 
     def __init__(self, B: int, capacity: int, device=None):
-        device = device or torch.device("cuda", torch.cuda.current_device())
+        device = torch.device("cuda" if device is None else device)
         new = lambda n, dtype: torch.empty(n, dtype=dtype, device=device)  # noqa: E731
-        self.cu_new = new(B + 1, torch.int64)
-        self.slot, self.pos = new(capacity, torch.int64), new(capacity, torch.int64)
-        self.row, self.status = new(capacity, torch.int32), new(B, torch.int32)
+        self._tensors = (new(B + 1, torch.int64), new(capacity, torch.int64),
+                         new(capacity, torch.int64), new(capacity, torch.int32),
+                         new(B, torch.int32))
+        if not self._tensors[0].is_cuda:
+            raise ValueError("a PagedBatch lies on a CUDA device")
+        self._shape = B, capacity, self._tensors[0].get_device()
+        self._addresses = tuple(t.data_ptr() for t in self._tensors)
+
+    cu_new = property(lambda self: self._tensors[0])
+    slot = property(lambda self: self._tensors[1])
+    pos = property(lambda self: self._tensors[2])
+    row = property(lambda self: self._tensors[3])
+    status = property(lambda self: self._tensors[4])
 
 
 def sparse_attn_paged_plan(length, n_new, block_table, free_pages, free_count, page_size: int,
@@ -396,42 +420,40 @@ def sparse_attn_paged_plan(length, n_new, block_table, free_pages, free_count, p
     if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda \
             or block_table.dim() != 2:
         raise ValueError("block_table must be a CUDA int32 [B, max_pages] tensor")
-    dev, (B, M) = block_table.device, block_table.shape
-    length_out = length if length_out is None else length_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    i64, i32, cap = torch.int64, torch.int32, batch.slot.numel()
+    B, M = shape = block_table.shape
+    dev, i64, i32 = block_table.get_device(), torch.int64, torch.int32
+    if batch._shape[0] != B or batch._shape[2] != dev:
+        raise ValueError(f"batch must be made for {B} requests on cuda:{dev}")
+    n_stack = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
+    len_p = _array(length, "length", i64, (B,), dev)
+    count_p = _array(free_count, "free_count", i64, (1,), dev)
     d = SaPagedStep(
-        B, M, int(page_size), cap, free_pages.numel(),
-        _array(length, "length", i64, (B,), dev), _array(n_new, "n_new", i32, (B,), dev),
-        _array(block_table, "block_table", i32, (B, M), dev),
-        _array(free_pages, "free_pages", i32, (free_pages.numel(),), dev),
-        _array(free_count, "free_count", i64, (1,), dev),
-        _array(length_out, "length_out", i64, (B,), dev),
-        _array(free_count_out, "free_count_out", i64, (1,), dev),
-        _array(batch.cu_new, "cu_new", i64, (B + 1,), dev),
-        _array(batch.slot, "slot", i64, (cap,), dev), _array(batch.pos, "pos", i64, (cap,), dev),
-        _array(batch.row, "row", i32, (cap,), dev), _array(batch.status, "status", i32, (B,), dev))
-    _check(_call_on(dev, stream, lambda s: _lib.sparse_attn_paged_plan(ctypes.byref(d), s)),
-           "sparse_attn_paged_plan")
+        B, M, page_size, batch._shape[1], n_stack, len_p, _array(n_new, "n_new", i32, (B,), dev),
+        _array(block_table, "block_table", i32, shape, dev),
+        _array(free_pages, "free_pages", i32, (n_stack,), dev), count_p,
+        len_p if length_out is None else _array(length_out, "length_out", i64, (B,), dev),
+        count_p if free_count_out is None else
+        _array(free_count_out, "free_count_out", i64, (1,), dev), *batch._addresses)
+    _call_on(dev, stream, "sparse_attn_paged_plan", _lib.sparse_attn_paged_plan, ctypes.byref(d))
     return batch
 
 
 def _token_rows(t, name: str, cache: PagedCache):
     """New rows [N, Hkv, D] or [N, Hkv, 1, D] with any stride between tokens:
     the descriptor and that stride."""
-    c = cache._desc
-    if not isinstance(t, torch.Tensor) or t.device != cache.device:
+    H, D = cache._heads, cache._dim
+    if not isinstance(t, torch.Tensor) or t.get_device() != cache._index:
         raise ValueError(f"{name} must be a tensor on {cache.device}")
     if t.dim() == 4 and t.shape[2] == 1:
         t = t[:, :, 0]
-    if t.dim() != 3 or t.shape[1:] != (c.Hkv, c.D) or t.stride(2) != 1 \
-            or (c.Hkv > 1 and t.stride(1) != c.D):
-        raise ValueError(f"{name} must be [N, {c.Hkv}, {c.D}] with contiguous heads")
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 3 or shape[1] != H or shape[2] != D or stride[2] != 1 \
+            or (H > 1 and stride[1] != D):
+        raise ValueError(f"{name} must be [N, {H}, {D}] with contiguous heads")
     dt = _PAGED_DTYPES.get(t.dtype, -1)
     if dt == SA_E4M3:
         raise ValueError(f"{name}: new rows are bf16 or fp32")
-    stride = t.stride(0) if t.shape[0] > 1 else c.Hkv * c.D
-    return SaTensor(t.data_ptr(), dt, t.shape[0], c.Hkv, 1, c.D), stride
+    return SaTensor(t.data_ptr(), dt, shape[0], H, 1, D), stride[0] if shape[0] > 1 else H * D
 
 
 def sparse_attn_paged_append(k_new, v_new, cache: PagedCache, slot, stream=None):
@@ -440,20 +462,17 @@ def sparse_attn_paged_append(k_new, v_new, cache: PagedCache, slot, stream=None)
     are skipped.  bf16 rows are rounded to 8 bits, one scale per row, for a
     float8_e4m3fn cache."""
     (tk, sk), (tv, sv) = _token_rows(k_new, "k_new", cache), _token_rows(v_new, "v_new", cache)
+    ps = _array(slot, "slot", torch.int64, (tk.B,), cache._index)
     if tk.B == 0 and tv.B == 0:
         return
-    ps = _array(slot, "slot", torch.int64, (tk.B,), cache.device)
-    _check(_call_on(cache.device, stream,
-                    lambda s: _lib.sparse_attn_paged_append(
-                        ctypes.byref(tk), sk, ctypes.byref(tv), sv, ps,
-                        ctypes.byref(cache._desc), s)),
-           "sparse_attn_paged_append")
+    _call_on(cache._index, stream, "sparse_attn_paged_append", _lib.sparse_attn_paged_append,
+             ctypes.byref(tk), sk, ctypes.byref(tv), sv, ps, cache._ref)
 
 
 def sparse_attn_paged_decode_workspace_size(q, cache: PagedCache, g: Graph) -> int:
     tq = _tensor(q, "q")
-    return int(_lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(tq),
-                                                            ctypes.byref(cache._desc), g.handle))
+    return int(_lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(tq), cache._ref,
+                                                            g.handle))
 
 
 def sparse_attn_paged_decode(q, cache: PagedCache, block_table, pos, g: Graph, scale: float,
@@ -463,34 +482,33 @@ def sparse_attn_paged_decode(q, cache: PagedCache, block_table, pos, g: Graph, s
     t's is row t) of block_table (int32 [rows, max_pages]).  Returns (out
     [N, H, 1, D], lse fp32 [N, H])."""
     tq = _tensor(q, "q")
-    N, H, _, D = q.shape
-    dev = cache.device
-    if q.device != dev:
-        raise ValueError(f"q must be on {dev}")
+    N, H, D, dev = tq.B, tq.H, tq.D, cache._index
+    if q.get_device() != dev:
+        raise ValueError(f"q must be on {cache.device}")
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be a CUDA int32 [rows, max_pages] tensor")
+    rows, M = shape = block_table.shape
     out = torch.empty_like(q) if out is None else out
     if lse is None:
-        lse = torch.empty((N, H), dtype=torch.float32, device=dev)
+        lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
+    out_p = _array(out, "out", q.dtype, q.shape, dev)
+    lse_p = _array(lse, "lse", torch.float32, (N, H), dev)
+    table_p = _array(block_table, "block_table", torch.int32, shape, dev)
+    pos_p = _array(pos, "pos", torch.int64, (N,), dev)
+    row_p = None if row is None else _array(row, "row", torch.int32, (N,), dev)
     if N == 0:
         return out, lse
-    _array(out, "out", q.dtype, q.shape, dev)
-    _array(lse, "lse", torch.float32, (N, H), dev)
-    _array(block_table, "block_table", torch.int32, block_table.shape, dev)
-    _array(pos, "pos", torch.int64, (N,), dev)
-    if row is not None:
-        _array(row, "row", torch.int32, (N,), dev)
     if workspace is None:
-        n = sparse_attn_paged_decode_workspace_size(q, cache, g)
-        workspace = torch.empty(n, dtype=torch.uint8, device=dev) if n else None
-    to = SaTensor(out.data_ptr(), tq.dtype, N, H, 1, D)
-    _check(_call_on(dev, stream, lambda s: _lib.sparse_attn_paged_decode(
-        ctypes.byref(tq), ctypes.byref(cache._desc), block_table.data_ptr(),
-        block_table.shape[0], block_table.shape[1], None if row is None else row.data_ptr(),
-        pos.data_ptr(), g.handle, float(scale), ctypes.byref(to), lse.data_ptr(),
-        None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), s)),
-        "sparse_attn_paged_decode")
+        size = _lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(tq), cache._ref, g.handle)
+        if size:
+            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on {cache.device}")
+    ws_p, ws_n = (None, 0) if workspace is None else (
+        workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    _call_on(dev, stream, "sparse_attn_paged_decode", _lib.sparse_attn_paged_decode,
+             ctypes.byref(tq), cache._ref, table_p, rows, M, row_p, pos_p, g.handle, float(scale),
+             ctypes.byref(SaTensor(out_p, tq.dtype, N, H, 1, D)), lse_p, ws_p, ws_n)
     return out, lse
 
 

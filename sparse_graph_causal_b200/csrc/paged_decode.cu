@@ -251,9 +251,10 @@ struct MmaTile {
     static constexpr bool k8 = sizeof(T) == 1;
     static constexpr int D = kD, NQ = 8 * NB;
     static constexpr int RB = D * (int)sizeof(T);          // bytes of a row
-    static constexpr int KT = RB == 256 || (!k8 && D == 64) ? 16 : 32;
-    static constexpr int kStages = RB == 32 ? 4 : 3, kWarps = 8;
-    static constexpr int kOcc = D == 128 || NB == 2 ? 1 : 2;
+    static constexpr int KT = RB >= 128 ? 16 : 32;
+    static constexpr int kStages = RB == 256 || (!k8 && D == 32) ? 3 : 4;
+    static constexpr int kWarps = RB == 256 || NB == 2 || D == 32 ? 8 : 12;
+    static constexpr int kOcc = D == 32 && NB == 1 ? 2 : 1;
     static constexpr int KP = RB / 4 < 16 ? RB / 4 : 16, KN = RB / 4 / KP;
     static constexpr int VP = RB / 8 < 16 ? RB / 8 : 16, VN = RB / 8 / VP;
     static constexpr int VE = VP / (int)sizeof(T);
@@ -525,14 +526,15 @@ struct MmaTile {
 template <int kD, int NB>
 struct FmaTile {
     using Out = float;
-    static constexpr int D = kD, NQ = 8 * NB, RB = 4 * D, KT = 16;
-    static constexpr int kStages = D == 32 || NB == 2 ? 2 : 3, kWarps = D == 128 ? 4 : 8;
-    static constexpr int kOcc = D == 32 && NB == 1 ? 2 : 1;
+    static constexpr int D = kD, NQ = 8 * NB, RB = 4 * D;
+    static constexpr int KT = 1024 / D;   // 8 KB of keys and values
+    static constexpr int kStages = D == 128 || NB == 2 ? 2 : 3, kWarps = 8, kOcc = 1;
     static constexpr int kStageBytes = 2 * KT * RB;
     static constexpr int kOwnBytes = NQ * D * 4 + NQ * KT * 4;  // queries and probabilities
     static constexpr int C = D / 4;       // 16-byte pieces of a row
     static constexpr int KG = 32 / C;     // keys side by side in the value sum
     static constexpr int KE = KT / KG;    // keys of a lane
+    static_assert(KE == 8, "two groups of four");
 
     int lane, gq;
     float *qs, *ps;
@@ -576,13 +578,14 @@ struct FmaTile {
     }
 
     __device__ __forceinline__ void tile(const uint8_t *stage, uint32_t mask) {
-        const int key = lane & 15, part = lane >> 4;
+        const int key = lane % KT, part = lane / KT;  // 32 columns of a key
         float s[NQ];
 #pragma unroll
         for (int x = 0; x < NQ; ++x) s[x] = 0.f;
-#pragma unroll 4
-        for (int c0 = 0; c0 < C / 2; ++c0) {
-            const int c = part * (C / 2) + c0;
+#pragma unroll
+        for (int c0 = 0; c0 < 8; ++c0) {
+            // (parts two pieces apart: different banks for the queries)
+            const int c = part * 8 + ((c0 + 2 * part) & 7);
             const float4 k =
                 *reinterpret_cast<const float4 *>(stage + key * RB + ((c ^ (key & 7)) << 4));
 #pragma unroll
@@ -596,11 +599,13 @@ struct FmaTile {
 #pragma unroll
         for (int x = 0; x < NQ; ++x)
             if (x < gq) {
-                float z = s[x] + __shfl_xor_sync(kFull, s[x], 16);
+                float z = s[x];
+#pragma unroll
+                for (int o = KT; o < 32; o <<= 1) z += __shfl_xor_sync(kFull, z, o);
                 if (!on) z = -INFINITY;
                 float top = z;
 #pragma unroll
-                for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+                for (int o = KT / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
                 top = fmaxf(top, m[x]);
                 const float base = finite_base(top), fall = ex2(m[x] - base);
                 const float p = ex2(z - base);
@@ -643,7 +648,7 @@ struct FmaTile {
 #pragma unroll
         for (int x = 0; x < NQ; ++x) {
 #pragma unroll
-            for (int o = 8; o; o >>= 1) l[x] += __shfl_xor_sync(kFull, l[x], o);
+            for (int o = KT / 2; o; o >>= 1) l[x] += __shfl_xor_sync(kFull, l[x], o);
 #pragma unroll
             for (int o = C; o < 32; o <<= 1) {
                 acc[x].x += __shfl_xor_sync(kFull, acc[x].x, o);
@@ -840,17 +845,26 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
         n * a.H + b.first, b.gq);
 }
 
+// a / b of non-negative numbers: in 32 bits, an eighth of the time, if they fit.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+    return a / b;
+}
+
 // Equal shares of `total` tiles.
 struct Shares {
     int64_t base, rem;
-    __device__ Shares(int64_t total, int64_t n) : base(total / n), rem(total % n) {}
+    __device__ Shares(int64_t total, int64_t n) : base(quotient(total, n)), rem(total - base * n) {}
     __device__ int64_t begin(int64_t w) const { return w * base + (w < rem ? w : rem); }
     __device__ int64_t of(int64_t x) const {
         const int64_t big = rem * (base + 1);
-        return x < big ? x / (base + 1) : rem + (x - big) / base;
+        return x < big ? quotient(x, base + 1) : rem + quotient(x - big, base);
     }
 };
 
+// What the start of a row costs a warp (positions, pages and the first copies
+// one after the other, then the merge), in tiles.  The shares count it.
+constexpr int kRowStart = 3;
 // Fewest tiles worth a warp: below, a share is mostly its own start and merge.
 constexpr int kLeastTiles = 4;
 
@@ -866,17 +880,20 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     __shared__ int64_t s_unit[NW][2];    // the cut rows of each warp: one it goes on with, one
     __shared__ int64_t s_end[NW];        //   it starts; the end of the latter
     __shared__ int s_ends[NW];           // the former ends here
+    __shared__ int s_group[2 * NW];      // rows cut in this CTA: first part, how many
+    __shared__ int s_groups;
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t U = (int64_t)a.Hkv * a.QB;
     auto tiles_of = [&](int32_t deg) { return max(1, (deg + KT - 1) / KT); };
+    auto cost_of = [&](int32_t deg) { return tiles_of(deg) + kRowStart; };
 
     // how many tiles there are, and where each run of rows begins
     const int64_t per = (a.N + NT - 1) / NT;
     {
         int64_t own = 0;
         for (int64_t n = tid * per; n < min(a.N, (tid + 1) * per); ++n)
-            own += tiles_of(token_of(a, g, n).deg);
+            own += cost_of(token_of(a, g, n).deg);
         int64_t x = own;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -892,8 +909,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
         __syncthreads();
     }
     const int64_t total = s_start[NT] * U;
-    const int64_t want = (total + (int64_t)kLeastTiles * gridDim.x - 1) /
-                         ((int64_t)kLeastTiles * gridDim.x);
+    const int64_t want = quotient(total, (int64_t)kLeastTiles * gridDim.x) + 1;
     const int nw = want < NW ? (int)want : NW;  // warps at work in each CTA
     const Shares shares(total, (int64_t)nw * gridDim.x);
     const int64_t W = (int64_t)blockIdx.x * nw + warp;
@@ -902,7 +918,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     uint8_t *own = mem + warp * M::kBytes;
     if (x < x_end) {
         // the row of tile x
-        const int64_t y = x / U;
+        const int64_t y = quotient(x, U);
         int lo = 0, hi = NT - 1;  // last run that begins at or before y
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -913,7 +929,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
         if (per > 1) {
             for (;; n += 32) {
                 const int64_t mine = n + lane;
-                int64_t z = mine < a.N ? tiles_of(token_of(a, g, mine).deg) : 0;
+                int64_t z = mine < a.N ? cost_of(token_of(a, g, mine).deg) : 0;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t up = __shfl_up_sync(kFull, z, o);
@@ -932,32 +948,36 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
         }
         n = min(n, a.N - 1);
         Token t = token_of(a, g, n);
-        int64_t in_row = x - before * U;
+        const int64_t in_row = x - before * U;
         int32_t tiles = tiles_of(t.deg);
-        int32_t u = (int32_t)(in_row / tiles);
-        int32_t tile0 = (int32_t)(in_row - (int64_t)u * tiles);
+        int32_t u = (int32_t)quotient(in_row, tiles + kRowStart);
+        int32_t from = (int32_t)(in_row - (int64_t)u * (tiles + kRowStart));
         Tile tile;
         while (true) {
-            if (t.bad && lane == 0) atomicOr(a.err, SA_DEVERR_BOUNDS);
-            const int32_t run = (int32_t)min((int64_t)(tiles - tile0), x_end - x);
-            const Block b = block_of<Tile::NQ>(a, u);
-            tile.begin(a, own + M::kRing, n, b.first, b.gq);
-            run_edges(tile, a, g, t, b.kvh, tile0 * KT, min(t.deg, (tile0 + run) * KT), own);
-            const bool goes_on = tile0 > 0, ends = tile0 + run == tiles;
-            if (!goes_on && ends) {
-                write_out(tile, a, n * a.H + b.first, b.gq);
-            } else {
-                const int which = goes_on ? 0 : 1;
-                write_part(tile, a.warp_part + (W * 2 + which) * PF);
-                if (lane == 0) {
-                    s_unit[warp][which] = n * U + u;
-                    if (goes_on) s_ends[warp] = ends;
-                    else s_end[warp] = x + tiles;
+            // [from, to) of the row's cost; its first kRowStart are its start
+            const int32_t to = (int32_t)min((int64_t)(tiles + kRowStart), from + (x_end - x));
+            const int32_t tile0 = max(from - kRowStart, 0), tile1 = to - kRowStart;
+            if (tile1 > 0) {
+                if (t.bad && lane == 0) atomicOr(a.err, SA_DEVERR_BOUNDS);
+                const Block b = block_of<Tile::NQ>(a, u);
+                tile.begin(a, own + M::kRing, n, b.first, b.gq);
+                run_edges(tile, a, g, t, b.kvh, tile0 * KT, min(t.deg, tile1 * KT), own);
+                const bool goes_on = tile0 > 0, ends = tile1 == tiles;
+                if (!goes_on && ends) {
+                    write_out(tile, a, n * a.H + b.first, b.gq);
+                } else {
+                    const int which = goes_on ? 0 : 1;
+                    write_part(tile, a.warp_part + (W * 2 + which) * PF);
+                    if (lane == 0) {
+                        s_unit[warp][which] = n * U + u;
+                        if (goes_on) s_ends[warp] = ends;
+                        else s_end[warp] = x + (tiles + kRowStart - from);
+                    }
                 }
             }
-            x += run;
+            x += to - from;
             if (x >= x_end) break;
-            tile0 = 0;
+            from = 0;
             if (++u == U) {
                 u = 0;
                 t = token_of(a, g, ++n);
@@ -967,42 +987,41 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     }
     __syncthreads();
 
-    // the CTA's cut rows, in order: each is merged over its warps
+    // the CTA's cut rows, in order: parts of one row are neighbours
+    if (warp == 0) {
+        const int64_t unit = lane < 2 * NW ? s_unit[lane >> 1][lane & 1] : -1;
+        const unsigned there = __ballot_sync(kFull, unit >= 0);
+        const unsigned below = there & ((1u << lane) - 1);
+        const int64_t before = __shfl_sync(kFull, unit, below ? 31 - __clz(below) : lane);
+        const bool first = unit >= 0 && (!below || before != unit);
+        const unsigned firsts = __ballot_sync(kFull, first);
+        const unsigned after = firsts & ~((2u << lane) - 1);
+        const unsigned upto = after ? (1u << (__ffs(after) - 1)) - 1 : kFull;
+        if (first)
+            s_group[__popc(firsts & ((1u << lane) - 1))] =
+                lane | __popc(there & upto & ~((1u << lane) - 1)) << 8;
+        if (lane == 0) s_groups = __popc(firsts);
+    }
+    __syncthreads();
     int4 cut = make_int4(-1, -1, 0, 0);
-    for (int i = 0; i < 2 * NW;) {
-        const int64_t unit = s_unit[i >> 1][i & 1];
-        if (unit < 0) {
-            ++i;
-            continue;
-        }
-        const bool starts = i & 1;
-        const int first = i;
-        int count = 0, last = i;
-        // (entries of other rows, or none, lie between a row's parts only where
-        // they are empty)
-        for (; i < 2 * NW; ++i) {
-            const int64_t other = s_unit[i >> 1][i & 1];
-            if (other == unit) last = i, ++count;
-            else if (other >= 0) break;
-        }
-        const bool ends = !(last & 1) && s_ends[last >> 1];
-        const int64_t n = unit / U;
+    for (int i = 0; i < s_groups; ++i) {
+        const int first = s_group[i] & 255, count = s_group[i] >> 8, w0 = first >> 1;
+        const bool starts = first & 1;
+        // (a part of its own start alone goes on elsewhere)
+        const int last = w0 + count - 1;
+        const bool ends = (!starts || count > 1) && s_ends[last];
+        const int64_t unit = s_unit[w0][first & 1], n = quotient(unit, U);
         const Block b = block_of<Tile::NQ>(a, (int32_t)(unit - n * U));
         float *to = starts && ends ? nullptr
                                    : a.cta_part + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * PF;
-        // parts of one row: slot 1 of the warp it starts in, then slots 0
-        const int w0 = first >> 1;
+        // slot 1 of the warp it starts in, then slots 0
+        const float *parts = a.warp_part + ((int64_t)blockIdx.x * nw + w0) * 2 * PF;
         merge_parts<Tile>(
-            a,
-            [&](int k) {
-                const int slot = starts && k == 0 ? 1 : 0;
-                return (const float *)a.warp_part +
-                       (((int64_t)blockIdx.x * nw + w0 + k) * 2 + slot) * PF;
-            },
-            count, to, n * a.H + b.first, b.gq);
+            a, [&](int k) { return parts + (2 * k + (starts && k == 0 ? 1 : 0)) * PF; }, count, to,
+            n * a.H + b.first, b.gq);
         if (starts && !ends)
             cut = make_int4((int)(unit & 0xffffffff), (int)(unit >> 32),
-                            (int)(shares.of(s_end[first >> 1] - 1) / nw), 0);
+                            (int)quotient(shares.of(s_end[w0] - 1), nw), 0);
     }
     if (tid == 0) a.cut[blockIdx.x] = cut;
 }
@@ -1021,7 +1040,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) 
     const int4 cut = __ldcg(a.cut + blockIdx.x);
     const int64_t unit = (int64_t)(uint32_t)cut.x | ((int64_t)cut.y << 32);
     if (unit < 0) return;
-    const int64_t U = (int64_t)a.Hkv * a.QB, n = unit / U;
+    const int64_t U = (int64_t)a.Hkv * a.QB, n = quotient(unit, U);
     const Block b = block_of<NQ>(a, (int32_t)(unit - n * U));
     const int q = blockIdx.y, c = threadIdx.x % C, r = threadIdx.x / C;
     if (q >= b.gq) return;
