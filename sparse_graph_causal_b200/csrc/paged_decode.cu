@@ -92,6 +92,10 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, bool o
                      : "memory");
 }
 
+__device__ __forceinline__ void copy_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 __device__ __forceinline__ void copies_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -137,10 +141,12 @@ __device__ __forceinline__ uint32_t half_bits(__half2 h) {
     return *reinterpret_cast<uint32_t *>(&h);
 }
 
-// Two 8-bit values as two fp16 ones (exact).
-__device__ __forceinline__ uint32_t widen(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | ((uint32_t)h.y << 16);
+// Four 8-bit values as fp16 ones (exact): bytes 0, 1 and bytes 2, 3.
+__device__ __forceinline__ void widen(uint32_t four, uint32_t &lo, uint32_t &hi) {
+    asm("{.reg .b16 x, y; mov.b32 {x, y}, %2; cvt.rn.f16x2.e4m3x2 %0, x; "
+        "cvt.rn.f16x2.e4m3x2 %1, y;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
 }
 
 // p0, p1 as 16-bit numbers and what their rounding leaves.
@@ -174,7 +180,7 @@ struct DecodeArgs {
     float scale2;           // scale * log2(e)
     void *out;
     float *lse;
-    float *warp_part, *cta_part;  // slots [warp or CTA][2] of partial rows
+    float *warp_part, *cta_part;  // partial rows: slots [warp], [CTA][2]
     int4 *cut;                    // per CTA: the row that starts there and is cut
     int *err;
 };
@@ -205,10 +211,15 @@ __device__ __forceinline__ Token token_of(const DecodeArgs &a, const GraphView &
     return t;
 }
 
-// A partial row: m[NQ], l[NQ], acc[NQ][D].
+// A partial row: m[NQ], l[NQ], acc[NQ][D], fours of columns permuted within 32
+// so that the lanes of a matrix product's result, eight columns and a row
+// apart, meet different banks.
 template <int NQ, int D>
 struct Part {
     static constexpr int kFloats = NQ * (D + 2);
+    __device__ __forceinline__ static int place(int q, int four) {
+        return 2 * NQ + q * D + 4 * (four ^ ((((four >> 3) << 1) | (q & 1)) & 7));
+    }
 };
 
 // Joins two softmax states.
@@ -231,8 +242,9 @@ struct State {
 };
 
 __device__ __forceinline__ float4 divided(float4 o, float l) {
+    const float r = 1.f / l;
     if (l == 0.f) return make_float4(0.f, 0.f, 0.f, 0.f);
-    return make_float4(o.x / l, o.y / l, o.z / l, o.w / l);
+    return make_float4(o.x * r, o.y * r, o.z * r, o.w * r);
 }
 
 __device__ __forceinline__ void store4(__nv_bfloat16 *p, float4 o) {
@@ -251,8 +263,8 @@ struct MmaTile {
     static constexpr bool k8 = sizeof(T) == 1;
     static constexpr int D = kD, NQ = 8 * NB;
     static constexpr int RB = D * (int)sizeof(T);          // bytes of a row
-    static constexpr int KT = RB >= 128 ? 16 : 32;
-    static constexpr int kStages = RB == 256 || (!k8 && D == 32) ? 3 : 4;
+    static constexpr int KT = RB == 256 ? 16 : 32;
+    static constexpr int kStages = RB == 32 ? 4 : RB == 128 && NB == 1 ? 2 : 3;
     static constexpr int kWarps = RB == 256 || NB == 2 || D == 32 ? 8 : 12;
     static constexpr int kOcc = D == 32 && NB == 1 ? 2 : 1;
     static constexpr int KP = RB / 4 < 16 ? RB / 4 : 16, KN = RB / 4 / KP;
@@ -336,19 +348,27 @@ struct MmaTile {
 
     // Start the copies of a tile: at[] are the offsets of its rows in the
     // cache, in bytes, -1 for none.  A row's lanes are neighbours.
-    __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage,
-                                         const int64_t *at) const {
+    __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage, const int64_t *at,
+                                         bool every) const {
         constexpr int L = RB / 16, R = 32 / L;
         const int ln = threadIdx.x & 31, sub = ln % L, h = ln / L;
         const uint32_t dst = smem_addr(stage);
+        const uint8_t *k = (const uint8_t *)a.k + sub * 16, *v = (const uint8_t *)a.v + sub * 16;
+        if (every) {
 #pragma unroll
-        for (int x = 0; x < KT / R; ++x) {
-            const int64_t o = at[x * R + h];
-            const bool on = o >= 0;
-            const int64_t src = (on ? o : 0) + sub * 16;
-            copy_async<16>(dst + key_place(x * R + h, sub), (const uint8_t *)a.k + src, on);
-            copy_async<16>(dst + KT * RB + value_place(x * R + h, sub), (const uint8_t *)a.v + src,
-                           on);
+            for (int x = 0; x < KT / R; ++x) {
+                const int64_t o = at[x * R + h];
+                copy_async16(dst + key_place(x * R + h, sub), k + o);
+                copy_async16(dst + KT * RB + value_place(x * R + h, sub), v + o);
+            }
+        } else {
+#pragma unroll 1
+            for (int x = 0; x < KT / R; ++x) {
+                const int64_t o = at[x * R + h];
+                copy_async<16>(dst + key_place(x * R + h, sub), k + (o < 0 ? 0 : o), o >= 0);
+                copy_async<16>(dst + KT * RB + value_place(x * R + h, sub), v + (o < 0 ? 0 : o),
+                               o >= 0);
+            }
         }
         if constexpr (k8) {
             const uint32_t sdst = dst + 2 * KT * RB;
@@ -383,10 +403,13 @@ struct MmaTile {
                 qa[2] = qf[y][NB];
                 qa[1] = NB == 1 ? 0 : qf[y][NB - 1];
                 qa[3] = NB == 1 ? 0 : qf[y][2 * NB - 1];
-                if constexpr (k8)
-                    mma(s2[y & 1], qa, widen(w[y] & 0xffffu), widen(w[y] >> 16), T());
-                else
+                if constexpr (k8) {
+                    uint32_t b0, b1;
+                    widen(w[y], b0, b1);
+                    mma(s2[y & 1], qa, b0, b1, T());
+                } else {
                     mma(s2[y & 1], qa, w[2 * y], w[2 * y + 1], T());
+                }
             }
 #pragma unroll
             for (int y = 0; y < 4; ++y) s[x][y] = s2[0][y] + s2[1][y];
@@ -465,14 +488,10 @@ struct MmaTile {
                     uint32_t b0[4], b1[4];
                     constexpr int E = k8 ? 4 : 2;
                     if constexpr (k8) {
-                        const uint32_t u0 = __byte_perm(w[0][z], w[1][z], 0x5140);
-                        const uint32_t u1 = __byte_perm(w[0][z], w[1][z], 0x7362);
-                        const uint32_t u2 = __byte_perm(w[2][z], w[3][z], 0x5140);
-                        const uint32_t u3 = __byte_perm(w[2][z], w[3][z], 0x7362);
-                        b0[0] = widen(u0 & 0xffffu), b0[1] = widen(u0 >> 16);
-                        b0[2] = widen(u1 & 0xffffu), b0[3] = widen(u1 >> 16);
-                        b1[0] = widen(u2 & 0xffffu), b1[1] = widen(u2 >> 16);
-                        b1[2] = widen(u3 & 0xffffu), b1[3] = widen(u3 >> 16);
+                        widen(__byte_perm(w[0][z], w[1][z], 0x5140), b0[0], b0[1]);
+                        widen(__byte_perm(w[0][z], w[1][z], 0x7362), b0[2], b0[3]);
+                        widen(__byte_perm(w[2][z], w[3][z], 0x5140), b1[0], b1[1]);
+                        widen(__byte_perm(w[2][z], w[3][z], 0x7362), b1[2], b1[3]);
                     } else {
                         b0[0] = __byte_perm(w[0][z], w[1][z], 0x5410);
                         b0[1] = __byte_perm(w[0][z], w[1][z], 0x7632);
@@ -562,8 +581,8 @@ struct FmaTile {
 
     // Piece c of row r lies at place c ^ (r mod 8): eight lanes on eight rows
     // meet eight banks.
-    __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage,
-                                         const int64_t *at) const {
+    __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage, const int64_t *at,
+                                         bool) const {
         const uint32_t dst = smem_addr(stage);
         const int ln = threadIdx.x & 31;
 #pragma unroll
@@ -689,6 +708,7 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
     const int32_t n = (x1 - x0 + KT - 1) / KT;
     const int32_t p = (int32_t)t.p, window = (int32_t)t.e.lo - t.e.ndil;
 
+    constexpr uint32_t all = KT == 32 ? kFull : (1u << (KT & 31)) - 1;
     int32_t at = x0 + lane;      // the next edge of this lane to look up
     int32_t key = -1;            // its position
     int32_t page = -1, off = -1; // page and place of the one before
@@ -718,7 +738,7 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
                 ok ? (((int64_t)page * a.Hkv + kvh) * a.page.by + off) * Tile::RB : -1;
         if (lane == 0) masks[stage] = mask;
         __syncwarp();
-        tile.copy(a, mem + stage * Tile::kStageBytes, rows);
+        tile.copy(a, mem + stage * Tile::kStageBytes, rows, mask == all);
     };
     next_key();
     next_page();
@@ -756,51 +776,43 @@ template <typename Tile>
 __device__ __forceinline__ void write_part(Tile &tile, float *slot) {
     constexpr int NQ = Tile::NQ, D = Tile::D;
     tile.finish([&](int q, int d, float4 o, float m, float l) {
-        *reinterpret_cast<float4 *>(slot + 2 * NQ + q * D + d) = o;
+        *reinterpret_cast<float4 *>(slot + Part<NQ, D>::place(q, d / 4)) = o;
         if (d == 0) slot[q] = m, slot[NQ + q] = l;
     });
 }
 
-template <typename Tile>
-__device__ __forceinline__ void write_out(Tile &tile, const DecodeArgs &a, int64_t nh, int gq) {
-    using Out = typename Tile::Out;
-    tile.finish([&](int q, int d, float4 o, float m, float l) {
-        if (q >= gq) return;
-        State s;
-        s.m = m, s.l = l;
-        store4((Out *)a.out + (nh + q) * Tile::D + d, divided(o, l));
-        if (d == 0) a.lse[nh + q] = s.lse();
-    });
-}
-
-// Merge of partial rows by the whole CTA; slot(i) is the i-th of `count`.
-template <typename Tile, typename Slot>
-__device__ __forceinline__ void merge_parts(const DecodeArgs &a, Slot slot, int count, float *to,
-                                            int64_t nh, int gq) {
-    constexpr int NQ = Tile::NQ, D = Tile::D, C = D / 4;
-    for (int x = threadIdx.x; x < gq * C; x += blockDim.x) {
-        const int q = x / C, d = x % C * 4;
-        State s;
-        constexpr int kAtOnce = 8;
-        for (int i0 = 0; i0 < count; i0 += kAtOnce) {
-            float m[kAtOnce], l[kAtOnce];
-            float4 o[kAtOnce];
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i) {
-                const float *p = slot(min(i0 + i, count - 1));
-                m[i] = p[q], l[i] = p[NQ + q];
-                o[i] = *reinterpret_cast<const float4 *>(p + 2 * NQ + q * D + d);
-            }
-#pragma unroll
-            for (int i = 0; i < kAtOnce; ++i)
-                if (i0 + i < count) s.add(m[i], l[i], o[i]);
+// Merge of `count` parts of a row by `threads` threads, into another part or
+// (to == nullptr) the output.  Parts are entry `first` of the list, then every
+// second one from the next even.  (Not inlined: code that runs once costs its
+// fetch.)
+template <typename Out, int NQ, int D>
+__device__ __noinline__ void merge_parts(int tid, int threads, const float *const *list, int first,
+                                         int count, int gq, float *to, Out *out, float *lse) {
+    constexpr int C = D / 4;
+    auto part = [&](int k) { return list[k ? (first & ~1) + 2 * k : first]; };
+#pragma unroll 1
+    for (int x = tid; x < gq * C; x += threads) {
+        const int q = x / C, c = x % C;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) m = fmaxf(m, part(k)[q]);
+        const float base = finite_base(m);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int k = 0; k < count; ++k) {
+            const float *p = part(k);
+            const float w = ex2(p[q] - base);
+            const float4 y = *reinterpret_cast<const float4 *>(p + Part<NQ, D>::place(q, c));
+            l = fmaf(w, p[NQ + q], l);
+            o.x = fmaf(w, y.x, o.x), o.y = fmaf(w, y.y, o.y);
+            o.z = fmaf(w, y.z, o.z), o.w = fmaf(w, y.w, o.w);
         }
         if (to) {
-            *reinterpret_cast<float4 *>(to + 2 * NQ + q * D + d) = s.o;
-            if (d == 0) to[q] = s.m, to[NQ + q] = s.l;
+            *reinterpret_cast<float4 *>(to + Part<NQ, D>::place(q, c)) = o;
+            if (c == 0) to[q] = m, to[NQ + q] = l;
         } else {
-            store4((typename Tile::Out *)a.out + (nh + q) * D + d, divided(s.o, s.l));
-            if (d == 0) a.lse[nh + q] = s.lse();
+            store4(out + q * D + 4 * c, divided(o, l));
+            if (c == 0) lse[q] = l == 0.f ? -INFINITY : (base + lg2(l)) * kLn2;
         }
     }
 }
@@ -822,6 +834,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     paged_decode_direct(DecodeArgs a, GraphView g) {
     using M = Layout<Tile>;
     extern __shared__ __align__(128) uint8_t mem[];
+    __shared__ const float *s_part[2 * Tile::kWarps];
     const int U = a.Hkv * a.QB, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int64_t n = blockIdx.x / U;
     const Block b = block_of<Tile::NQ>(a, blockIdx.x % U);
@@ -834,15 +847,13 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     Tile tile;
     tile.begin(a, own + M::kRing, n, b.first, b.gq);
     run_edges(tile, a, g, t, b.kvh, x0, x1, own);
-    if (nw == 1) {
-        write_out(tile, a, n * a.H + b.first, b.gq);
-        return;
-    }
     write_part(tile, (float *)own);
+    if ((threadIdx.x & 31) == 0) s_part[2 * warp] = (float *)own;
     __syncthreads();
-    merge_parts<Tile>(
-        a, [&](int i) { return (const float *)(mem + i * M::kBytes); }, nw, nullptr,
-        n * a.H + b.first, b.gq);
+    const int64_t nh = n * a.H + b.first;
+    merge_parts<typename Tile::Out, Tile::NQ, Tile::D>(
+        threadIdx.x, blockDim.x, s_part, 0, nw, b.gq, nullptr,
+        (typename Tile::Out *)a.out + nh * Tile::D, a.lse + nh);
 }
 
 // a / b of non-negative numbers: in 32 bits, an eighth of the time, if they fit.
@@ -873,13 +884,15 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     paged_decode_split(DecodeArgs a, GraphView g) {
     using M = Layout<Tile>;
     constexpr int NW = Tile::kWarps, NT = 32 * NW, KT = Tile::KT;
-    constexpr int PF = M::P::kFloats;
+    constexpr int PF = M::P::kFloats, D = Tile::D;
+    using Out = typename Tile::Out;
     extern __shared__ __align__(128) uint8_t mem[];
     __shared__ int64_t s_start[NT + 1];  // row tiles before each thread's rows
     __shared__ int64_t s_sum[NW];
     __shared__ int64_t s_unit[NW][2];    // the cut rows of each warp: one it goes on with, one
     __shared__ int64_t s_end[NW];        //   it starts; the end of the latter
     __shared__ int s_ends[NW];           // the former ends here
+    __shared__ const float *s_part[2 * NW + 2 * NW];  // their parts; then each warp's ring
     __shared__ int s_group[2 * NW];      // rows cut in this CTA: first part, how many
     __shared__ int s_groups;
     asm volatile("griddepcontrol.launch_dependents;");
@@ -963,12 +976,21 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
                 tile.begin(a, own + M::kRing, n, b.first, b.gq);
                 run_edges(tile, a, g, t, b.kvh, tile0 * KT, min(t.deg, tile1 * KT), own);
                 const bool goes_on = tile0 > 0, ends = tile1 == tiles;
-                if (!goes_on && ends) {
-                    write_out(tile, a, n * a.H + b.first, b.gq);
+                // (the ring is free, but not for long if more rows follow)
+                const bool whole = !goes_on && ends, stays = x + (to - from) >= x_end;
+                float *part = whole || stays ? (float *)own : a.warp_part + W * PF;
+                write_part(tile, part);
+                if (whole) {
+                    const int64_t nh = n * a.H + b.first;
+                    if (lane == 0) s_part[2 * (NW + warp)] = part;
+                    __syncwarp();
+                    merge_parts<Out, Tile::NQ, D>(lane, 32, s_part, 2 * (NW + warp), 1, b.gq, nullptr,
+                                                  (Out *)a.out + nh * D, a.lse + nh);
+                    __syncwarp();
                 } else {
                     const int which = goes_on ? 0 : 1;
-                    write_part(tile, a.warp_part + (W * 2 + which) * PF);
                     if (lane == 0) {
+                        s_part[2 * warp + which] = part;
                         s_unit[warp][which] = n * U + u;
                         if (goes_on) s_ends[warp] = ends;
                         else s_end[warp] = x + (tiles + kRowStart - from);
@@ -1014,11 +1036,9 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
         const Block b = block_of<Tile::NQ>(a, (int32_t)(unit - n * U));
         float *to = starts && ends ? nullptr
                                    : a.cta_part + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * PF;
-        // slot 1 of the warp it starts in, then slots 0
-        const float *parts = a.warp_part + ((int64_t)blockIdx.x * nw + w0) * 2 * PF;
-        merge_parts<Tile>(
-            a, [&](int k) { return parts + (2 * k + (starts && k == 0 ? 1 : 0)) * PF; }, count, to,
-            n * a.H + b.first, b.gq);
+        const int64_t nh = n * a.H + b.first;
+        merge_parts<Out, Tile::NQ, D>(tid, NT, s_part, first, count, b.gq, to, (Out *)a.out + nh * D,
+                                      a.lse + nh);
         if (starts && !ends)
             cut = make_int4((int)(unit & 0xffffffff), (int)(unit >> 32),
                             (int)quotient(shares.of(s_end[w0] - 1), nw), 0);
@@ -1050,7 +1070,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) 
     for (int i = r; i < count; i += R) {
         const float *p = a.cta_part + (((int64_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * PF;
         s.add(__ldcg(p + q), __ldcg(p + NQ + q),
-              __ldcg(reinterpret_cast<const float4 *>(p + 2 * NQ + q * D + 4 * c)));
+              __ldcg(reinterpret_cast<const float4 *>(p + Part<NQ, D>::place(q, c))));
     }
     if (c == 0) s_m[r] = s.m, s_l[r] = s.l;
     s_o[r][c] = s.o;
@@ -1065,8 +1085,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) 
 
 // ------------------------------------------------------------------- host
 
-// Longest row that the direct way takes.
-constexpr int64_t kDirectKeys = 512;
+// Longest rows that the direct way takes, in bytes of keys and values.
+constexpr int64_t kDirectBytes = 384 << 10;
+
+bool is_direct(int64_t longest, const sa_paged_cache &c) {
+    const int64_t es = c.dtype == SA_FP32 ? 4 : c.dtype == SA_BF16 ? 2 : 1;
+    return longest * 2 * c.D * es <= kDirectBytes;
+}
 
 int64_t longest_row(const sa_graph_s *g) {
     int64_t n = g->kind == 0 ? (int64_t)g->W + g->n_off
@@ -1097,7 +1122,7 @@ auto with_tile(const sa_paged_cache &c, int64_t G, F f)
 struct Plan {
     int64_t ctas = 0, part_floats = 0, warps = 0;
     size_t bytes() const {
-        return ctas ? (size_t)(ctas * (warps + 1) * 2 * part_floats * 4 + ctas * 16) : 0;
+        return ctas ? (size_t)(ctas * (warps + 2) * part_floats * 4 + ctas * 16) : 0;
     }
 };
 
@@ -1111,11 +1136,12 @@ Plan split_plan(int sms) {
 }
 
 template <typename Tile>
-sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, void *workspace,
+sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, bool direct,
+                        void *workspace,
                         cudaStream_t s) {
     using M = Layout<Tile>;
     a.QB = (a.G + Tile::NQ - 1) / Tile::NQ;
-    if (longest <= kDirectKeys) {
+    if (direct) {
         const int64_t blocks = a.N * a.Hkv * a.QB;
         if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
         int nw = (int)((longest + Tile::KT - 1) / Tile::KT);
@@ -1132,7 +1158,7 @@ sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, void
     SA_CUDA_TRY(sa_sm_count(&sms));
     const Plan p = split_plan<Tile>(sms);
     a.warp_part = (float *)workspace;
-    a.cta_part = a.warp_part + p.ctas * p.warps * 2 * p.part_floats;
+    a.cta_part = a.warp_part + p.ctas * p.warps * p.part_floats;
     a.cut = (int4 *)(a.cta_part + p.ctas * 2 * p.part_floats);
     SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_split<Tile>, Tile::kWarps * M::kBytes));
     SA_LAUNCH("paged_decode", s,
@@ -1159,7 +1185,7 @@ sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, void
 size_t sa_paged_decode_workspace(const sa_tensor *q, const sa_paged_cache &c,
                                  const sa_graph_s *g) {
     int sms = 0;
-    if (longest_row(g) <= kDirectKeys || sa_sm_count(&sms) != cudaSuccess) return 0;
+    if (is_direct(longest_row(g), c) || sa_sm_count(&sms) != cudaSuccess) return 0;
     return with_tile(c, q->H / c.Hkv, [&](auto *t) {
         return split_plan<std::remove_pointer_t<decltype(t)>>(sms);
     }).bytes();
@@ -1192,11 +1218,12 @@ sa_status sa_paged_decode(const sa_tensor *q, const sa_paged_cache &c, const int
     a.err = sa_device_error_word();
     if (!a.err) return SA_ERR_CUDA;
     const GraphView gv = make_view(g);
+    const int64_t longest = longest_row(g);
     struct Result {
         sa_status st = SA_ERR_UNSUPPORTED;
     };
     return with_tile(c, a.G, [&](auto *t) {
-        return Result{launch_decode<std::remove_pointer_t<decltype(t)>>(a, gv, longest_row(g),
-                                                                       workspace, s)};
+        return Result{launch_decode<std::remove_pointer_t<decltype(t)>>(
+            a, gv, longest, is_direct(longest, c), workspace, s)};
     }).st;
 }
