@@ -204,7 +204,8 @@ sa_status sparse_attn_decode(const sa_tensor *q, const sa_tensor *k_cache,
  * A block table is DEVICE int32 [rows, max_pages]: entry [b, p] is the page
  * that holds the positions p * page_size ... of request b.  A page may stand
  * in several rows (a shared prompt).  max_pages * page_size, n_pages and
- * rows < 2^31 (max_pages * page_size <= 2^30 in sparse_attn_paged_decode).  A slot is page * page_size + row, the address of one cached
+ * rows < 2^31, Hkv <= 2^24 (and max_pages * page_size <= 2^30 in
+ * sparse_attn_paged_decode).  A slot is page * page_size + row, the address of one cached
  * position. */
 typedef struct {
     void *k, *v;

@@ -569,7 +569,7 @@ sa_status check_paged_cache(const sa_paged_cache *c) {
                             : c->k_scale || c->v_scale)
         return SA_ERR_INVALID_ARG;
     if (c->D != 32 && c->D != 64 && c->D != 128) return SA_ERR_UNSUPPORTED;
-    if (c->n_pages > kInt32Max || c->page_size > kInt32Max || c->Hkv > kInt32Max)
+    if (c->n_pages > kInt32Max || c->page_size > kInt32Max || c->Hkv > 1 << 24)
         return SA_ERR_UNSUPPORTED;
     return SA_OK;
 }

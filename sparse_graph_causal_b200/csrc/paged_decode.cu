@@ -48,6 +48,7 @@
 #include <type_traits>
 
 #include "gather_common.cuh"
+#include "paged_common.cuh"
 
 namespace {
 
@@ -56,23 +57,6 @@ using namespace gather;
 constexpr unsigned kFull = 0xffffffffu;
 
 // ------------------------------------------------------------------ pieces
-
-// n / P for 0 <= n < 2^31 as a product: with 2^(l-1) < P <= 2^l, M = ceil(2^(31+l) / P)
-// overshoots by e < P <= 2^l parts in 2^(31+l), and n e < 2^(31+l).
-struct Divide {
-    uint32_t mul, shift, by;
-};
-
-Divide make_divide(uint32_t by) {
-    uint32_t l = 0;
-    while ((1ull << l) < by) ++l;
-    const unsigned __int128 one = (unsigned __int128)1 << (31 + l);
-    return {(uint32_t)((one + by - 1) / by), 31 + l, by};
-}
-
-__device__ __forceinline__ uint32_t divide(uint32_t n, const Divide &d) {
-    return (uint32_t)(((uint64_t)n * d.mul) >> d.shift);
-}
 
 __device__ __forceinline__ uint32_t smem_addr(const void *p) {
     return (uint32_t)__cvta_generic_to_shared(p);
@@ -854,12 +838,6 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     merge_parts<typename Tile::Out, Tile::NQ, Tile::D>(
         threadIdx.x, blockDim.x, s_part, 0, nw, b.gq, nullptr,
         (typename Tile::Out *)a.out + nh * Tile::D, a.lse + nh);
-}
-
-// a / b of non-negative numbers: in 32 bits, an eighth of the time, if they fit.
-__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
-    if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-    return a / b;
 }
 
 // Equal shares of `total` tiles.

@@ -213,6 +213,34 @@ def test_append(sa, N, Hkv, D, page, dtype, wide):
         assert np.array_equal(g, w)
 
 
+def test_append_rounds_like_division(sa):
+    """Codes are the 8-bit roundings of correctly rounded 32-bit quotients: rows whose quotients
+    fall on the midpoints between codes, next to them, and everywhere else."""
+    N, Hkv, D, page = 8192, 2, 128, 64
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((2, N, Hkv, D)).astype(np.float32)
+    x *= np.exp2(rng.integers(-20, 20, (2, N, Hkv, 1))).astype(np.float32)
+    codes = paged_ref.E4M3
+    mids = np.concatenate([(codes[1:] + codes[:-1]) / 2, codes]).astype(np.float32)
+    half = x[:, : N // 2]
+    top = np.abs(half).max(-1, keepdims=True)
+    top = np.where(rng.random(top.shape) < 0.5, np.exp2(np.round(np.log2(top))) * 448, top)
+    half[:] = rng.choice(mids, half.shape) * rng.choice([-1, 1], half.shape) * top / 448
+    half[..., 0] = top[..., 0]
+    x = torch.from_numpy(x).bfloat16()
+    k, v = x.cuda()
+    shape = (N // page, Hkv, page, D)
+    kv = [torch.zeros(shape, device="cuda").to(TYPES["e4m3"]) for _ in range(2)]
+    scales = [torch.zeros(shape[:3], device="cuda") for _ in range(2)]
+    sa.sparse_attn_paged_append(k, v, sa.PagedCache(*kv, *scales),
+                                torch.arange(N, device="cuda"))
+    for new, pool, scale in zip(x, kv, scales):
+        y, s = paged_ref.quantise(new.float().numpy())
+        got = pool.transpose(1, 2).reshape(N, Hkv, D).float().cpu().numpy()
+        assert np.array_equal(scale.transpose(1, 2).reshape(N, Hkv).cpu().numpy(), s)
+        assert np.array_equal(got, y)
+
+
 def test_append_flags_slots_outside_the_cache(sa):
     n_pages, Hkv, page, D = 4, 2, 16, 64
     kp, vp = (torch.zeros((n_pages, Hkv, page, D), device="cuda", dtype=torch.bfloat16)
