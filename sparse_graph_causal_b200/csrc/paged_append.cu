@@ -29,7 +29,7 @@ struct AppendArgs {
     uint8_t *dst[2];
     float *scale[2];
     const int64_t *slot;
-    int64_t units;          // N * Hkv * L, 16-byte pieces of each of k, v
+    int64_t units;          // N * Hkv * L, pieces of each of k, v
     int64_t n_pages, Hkv;
     Divide per_token, page; // Hkv * L and P
     bool small;             // slots of the cache have 31 bits
@@ -46,35 +46,65 @@ __device__ __forceinline__ float quotient_rn(float x, float s, float r) {
     return fmaf(fmaf(-q, s, x), r, q);
 }
 
-// Eight bf16 values of a row whose largest magnitude has the bits `top`.
-__device__ __forceinline__ uint2 codes(uint4 x, uint32_t top, float &scale) {
-    const uint32_t b[4] = {x.x, x.y, x.z, x.w};
-    scale = top < 0x7f800000u ? __fdiv_rn(__uint_as_float(top), 448.f)
-                              : __uint_as_float(0x7fc00000u);
-    uint32_t code[2] = {0, 0};
-    if (scale > 0.f) {
-        const bool plain = scale >= 0x1p-60f && scale <= 0x1p60f;
-        const float r = __frcp_rn(scale);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float f0 = __uint_as_float(b[k] << 16);
-            const float f1 = __uint_as_float(b[k] & 0xffff0000u);
-            float2 y = make_float2(quotient_rn(f0, scale, r), quotient_rn(f1, scale, r));
-            if (!plain) y = make_float2(__fdiv_rn(f0, scale), __fdiv_rn(f1, scale));
-            const uint32_t c = __nv_cvt_float2_to_fp8x2(y, __NV_SATFINITE, __NV_E4M3);
-            code[k / 2] |= c << (16 * (k & 1));
-        }
-    }
-    return make_uint2(code[0], code[1]);
+// Two quotients as codes, the first in the low byte.
+__device__ __forceinline__ uint32_t code4(float y0, float y1, float y2, float y3) {
+    uint32_t c;
+    asm("{.reg .b16 x, y; cvt.rn.satfinite.e4m3x2.f32 x, %2, %1; "
+        "cvt.rn.satfinite.e4m3x2.f32 y, %4, %3; mov.b32 %0, {x, y};}"
+        : "=r"(c)
+        : "f"(y0), "f"(y1), "f"(y2), "f"(y3));
+    return c;
 }
 
-// L: threads per row (16 bytes of input each).
+// Scale and codes of a row in the ranges that the corrections do not cover
+// (not inlined: hardly ever run).
+__device__ __noinline__ float codes_by_division(float amax, const float *f, uint32_t *code) {
+    const float scale = amax < INFINITY ? __fdiv_rn(amax, 448.f) : __uint_as_float(0x7fc00000u);
+    for (int k = 0; k < 16; k += 4) {
+        float y[4];
+        for (int i = 0; i < 4; ++i) y[i] = scale > 0.f ? __fdiv_rn(f[k + i], scale) : 0.f;
+        code[k / 4] = code4(y[0], y[1], y[2], y[3]);
+    }
+    return scale;
+}
+
+// Sixteen bf16 values of a row whose largest magnitude is amax (or NaN).
+__device__ __forceinline__ uint4 codes(const uint4 (&x)[2], float amax, float &scale) {
+    float f[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint4 &y = x[k / 4];
+        const uint32_t b = k % 4 == 0 ? y.x : k % 4 == 1 ? y.y : k % 4 == 2 ? y.z : y.w;
+        f[2 * k] = __uint_as_float(b << 16);
+        f[2 * k + 1] = __uint_as_float(b & 0xffff0000u);
+    }
+    uint32_t c[4];
+    if (amax >= 0x1p-50f && amax <= 0x1p60f) {
+        scale = quotient_rn(amax, 448.f, 1.f / 448.f);
+        const float r = __frcp_rn(scale);
+#pragma unroll
+        for (int k = 0; k < 16; k += 4)
+            c[k / 4] = code4(quotient_rn(f[k], scale, r), quotient_rn(f[k + 1], scale, r),
+                             quotient_rn(f[k + 2], scale, r), quotient_rn(f[k + 3], scale, r));
+    } else {
+        float g[16];
+        uint32_t d[4];
+        for (int k = 0; k < 16; ++k) g[k] = f[k];
+        scale = codes_by_division(amax, g, d);
+        for (int k = 0; k < 4; ++k) c[k] = d[k];
+    }
+    return make_uint4(c[0], c[1], c[2], c[3]);
+}
+
+// L: threads per row, of 16 bytes of input each (32 where they are rounded, so
+// that the row's own work is shared by more values).
 template <int L, bool kQuant, int kUnits>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs a) {
     const int64_t base = (int64_t)blockIdx.x * (kThreads * kUnits);
     const int64_t t0 = quotient(base, a.per_token.by);  // token of the block's first piece
     const uint32_t r0 = (uint32_t)(base - t0 * a.per_token.by);
-    uint4 x[2][kUnits];
+    constexpr int V = kQuant ? 2 : 1;
+    uint4 x[2][kUnits][V];
     int64_t token[kUnits];
     uint32_t piece[kUnits];
     int64_t slot[kUnits];
@@ -88,9 +118,12 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         slot[i] = in ? a.slot[token[i]] : -1;
 #pragma unroll
         for (int w = 0; w < 2; ++w)
-            x[w][i] = in ? __ldg(reinterpret_cast<const uint4 *>(a.src[w] + token[i] * a.stride[w]) +
-                                 piece[i])
-                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int y = 0; y < V; ++y)
+                x[w][i][y] =
+                    in ? __ldg(reinterpret_cast<const uint4 *>(a.src[w] + token[i] * a.stride[w]) +
+                               (piece[i] * V + y))
+                       : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll
     for (int i = 0; i < kUnits; ++i) {
@@ -114,30 +147,28 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
         }
         if constexpr (!kQuant) {
             if (ok) {
-                reinterpret_cast<uint4 *>(a.dst[0])[dst * L + sub] = x[0][i];
-                reinterpret_cast<uint4 *>(a.dst[1])[dst * L + sub] = x[1][i];
+                reinterpret_cast<uint4 *>(a.dst[0])[dst * L + sub] = x[0][i][0];
+                reinterpret_cast<uint4 *>(a.dst[1])[dst * L + sub] = x[1][i][0];
             }
         } else {
-            // the largest magnitudes as integers: bf16 magnitudes order like
-            // their bits, and infinities and NaN stay on top
-            uint32_t top[2];
+            float top[2];  // largest magnitudes, NaN if there is one
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                const uint32_t b[4] = {x[w][i].x, x[w][i].y, x[w][i].z, x[w][i].w};
-                top[w] = 0;
+                const __nv_bfloat162 *b = reinterpret_cast<const __nv_bfloat162 *>(&x[w][i][0]);
+                __nv_bfloat162 m = __habs2(b[0]);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    top[w] = max(top[w], max((b[k] << 16) & 0x7fffffffu, b[k] & 0x7fff0000u));
+                for (int k = 1; k < 8; ++k) m = __hmax2_nan(m, __habs2(b[k]));
 #pragma unroll
                 for (int o = 1; o < L; o <<= 1)
-                    top[w] = max(top[w], __shfl_xor_sync(0xffffffffu, top[w], o));
+                    m = __hmax2_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
+                top[w] = __bfloat162float(__hmax_nan(m.x, m.y));
             }
             if (ok) {
 #pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     float scale;
-                    const uint2 code = codes(x[w][i], top[w], scale);
-                    reinterpret_cast<uint2 *>(a.dst[w])[dst * L + sub] = code;
+                    const uint4 code = codes(x[w][i], top[w], scale);
+                    reinterpret_cast<uint4 *>(a.dst[w])[dst * L + sub] = code;
                     if (sub == 0) a.scale[w][dst] = scale;
                 }
             }
@@ -155,14 +186,15 @@ sa_status launch_units(const AppendArgs &a, cudaStream_t s) {
     return SA_OK;
 }
 
-// Four pieces a thread keep enough loads in flight; few rows go one piece a
+// Four pieces a thread keep enough loads in flight (two where they are rounded:
+// the code of four outgrows the instruction cache); few rows go one piece a
 // thread, over more SMs.
 constexpr int64_t kFewUnits = 148 * 4 * kThreads;
 
 template <int L, bool kQuant>
 sa_status launch_append(const AppendArgs &a, cudaStream_t s) {
     return a.units <= kFewUnits ? launch_units<L, kQuant, 1>(a, s)
-                                : launch_units<L, kQuant, 4>(a, s);
+                                : launch_units<L, kQuant, kQuant ? 2 : 4>(a, s);
 }
 
 }  // namespace
@@ -172,7 +204,7 @@ sa_status sa_paged_append(const sa_tensor *k, int64_t k_stride, const sa_tensor 
                           cudaStream_t s) {
     const bool quant = c.dtype == SA_E4M3;
     const int es = k->dtype == SA_BF16 ? 2 : 4;
-    const int L = (int)(c.D * es / 16);
+    const int L = (int)(c.D * es / (quant ? 32 : 16));
     AppendArgs a = {};
     a.src[0] = (const uint8_t *)k->ptr;
     a.src[1] = (const uint8_t *)v->ptr;
@@ -191,11 +223,16 @@ sa_status sa_paged_append(const sa_tensor *k, int64_t k_stride, const sa_tensor 
     a.small = c.n_pages <= 0x7fffffffLL / c.page_size;
     a.err = sa_device_error_word();
     if (!a.err) return SA_ERR_CUDA;
-    switch (L) {
-        case 4: return quant ? launch_append<4, true>(a, s) : launch_append<4, false>(a, s);
-        case 8: return quant ? launch_append<8, true>(a, s) : launch_append<8, false>(a, s);
-        case 16: return quant ? launch_append<16, true>(a, s) : launch_append<16, false>(a, s);
-        case 32: return launch_append<32, false>(a, s);
-    }
+    if (quant) switch (L) {
+            case 2: return launch_append<2, true>(a, s);
+            case 4: return launch_append<4, true>(a, s);
+            case 8: return launch_append<8, true>(a, s);
+        }
+    else switch (L) {
+            case 4: return launch_append<4, false>(a, s);
+            case 8: return launch_append<8, false>(a, s);
+            case 16: return launch_append<16, false>(a, s);
+            case 32: return launch_append<32, false>(a, s);
+        }
     return SA_ERR_UNSUPPORTED;
 }
