@@ -13,227 +13,279 @@
 //           page, slot = page * P + pos mod P
 //
 // Nothing here is worth a byte of bandwidth (20 bytes a token, 40 a request):
-// the step is bound by its chain of dependent loads and by launches, so it is
-// one launch, a single CTA or one cluster.  Every CTA runs the scans of all
-// requests by itself (three 64-bit sums over 1,024 threads) and keeps what
-// the tokens need in its shared memory; then the CTAs share the tokens.  A
-// cluster barrier orders every read of the lengths before the writes of the
-// new ones (which may be the same array) and returned pages before taken ones.
+// the step is bound by its chain of dependent loads, barriers and launches, so
+// it is one launch, a single CTA or one cluster.  Every CTA runs the scans of
+// all requests by itself and keeps what the tokens need in its shared memory;
+// then the CTAs share the tokens, each found by bisection.  A cluster barrier
+// orders every read of the lengths before the writes of the new ones (which
+// may be the same array) and returned pages before taken ones.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "paged_common.cuh"
 #include "sa_internal.cuh"
 
 namespace {
 
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 1024;
-constexpr int kWarps = kThreads / 32;
+constexpr unsigned kFull = 0xffffffffu;
 
-// Inclusive prefix sum of one value per thread over the block.
-__device__ __forceinline__ int64_t block_scan(int64_t x, int64_t *s_part) {
+// Sums that stop at the largest value (they are compared with stack sizes).
+__device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
+    const uint32_t s = a + b;
+    return s < a ? 0xffffffffu : s;
+}
+
+// Inclusive prefix sums over the block of a 64-bit and a 32-bit value per
+// thread, with their totals; one barrier.  Returns whether any `flag` is set.
+template <int NW, typename A>
+__device__ __forceinline__ bool block_scan(A &x, uint32_t &y, A &x_all, uint32_t &y_all, bool flag,
+                                           A *s_x, uint32_t *s_y) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
-        if (lane >= o) x += y;
+        const A u = __shfl_up_sync(kFull, x, o);
+        const uint32_t v = __shfl_up_sync(kFull, y, o);
+        if (lane >= o) x += u, y = add_sat(y, v);
     }
-    __syncthreads();  // the last use of s_part is over
-    if (lane == 31) s_part[warp] = x;
-    __syncthreads();
-    if (warp == 0) {
-        int64_t p = s_part[lane];
+    if (lane == 31) s_x[warp] = x, s_y[warp] = y;
+    const bool any = __syncthreads_or(flag);
+    A u = lane < NW ? s_x[lane] : 0;
+    uint32_t v = lane < NW ? s_y[lane] : 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, p, o);
-            if (lane >= o) p += y;
-        }
-        s_part[lane] = p;
+    for (int o = 1; o < NW; o <<= 1) {
+        const A p = __shfl_up_sync(kFull, u, o);
+        const uint32_t q = __shfl_up_sync(kFull, v, o);
+        if (lane >= o) u += p, v = add_sat(v, q);
     }
-    __syncthreads();
-    return x + (warp ? s_part[warp - 1] : 0);
+    x_all = __shfl_sync(kFull, u, NW - 1);
+    y_all = __shfl_sync(kFull, v, NW - 1);
+    const A before = __shfl_sync(kFull, u, warp ? warp - 1 : 0);
+    const uint32_t before_y = __shfl_sync(kFull, v, warp ? warp - 1 : 0);
+    if (warp) x += before, y = add_sat(y, before_y);
+    return any;
 }
 
-// What the tokens of request b need, in shared memory: the end of its tokens
-// (clipped to capacity), its length, and its first new page counted from the
-// top of the stack (kRefused: it is not served).
+struct PlanArgs {
+    sa_paged_step s;
+    Divide page;
+};
+
+// First new page of a request counted from the top of the stack (a finished
+// one: where its pages go on the stack), or kRefused: it is not served.
 constexpr int kRefused = -1;
 
-// MAXPER: requests per thread (consecutive ones), kept in registers.
-template <int MAXPER>
-__global__ void __launch_bounds__(kThreads) paged_plan_kernel(sa_paged_step a) {
-    static_assert(kWarps == 32, "one warp scans the warps' sums");
+// NT threads; PER requests each (consecutive ones), kept in registers.
+template <int NT, int PER>
+__global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
+    const sa_paged_step &a = args.s;
+    constexpr int NW = NT / 32;
     extern __shared__ int32_t smem[];
-    __shared__ int64_t s_part[kWarps];
-    __shared__ int64_t s_free;
+    __shared__ int64_t s_x[NW];
+    __shared__ uint32_t s_y[NW], s_z[NW], s_w[NW], s_taken;
     const int B = (int)a.B, tid = threadIdx.x;
+    // the end of each request's tokens (clipped to capacity), its length (-1 -
+    // length if it is finished) and its first new page
     int32_t *s_end = smem, *s_len = smem + B, *s_new = smem + 2 * B;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ncta = (int)cluster.num_blocks();
-    const int64_t P = a.page_size, room = a.max_pages * P;
-    const int per = (B + kThreads - 1) / kThreads, b0 = tid * per;
+    const int64_t room = a.max_pages * a.page_size;
+    const uint32_t P = args.page.by;
+    const int b0 = tid * PER;
+    // ceil(x / P) for 0 <= x <= room < 2^31
+    auto pages = [&](int64_t x) { return x ? divide((uint32_t)x - 1, args.page) + 1 : 0; };
 
-    int64_t len[MAXPER];
-    int32_t nn[MAXPER];
-    if (tid == 0) s_free = *a.free_count;
-    int64_t tokens = 0, back = 0;
+    int64_t len[PER];
+    int32_t nn[PER];
+    const int64_t count = *a.free_count;
 #pragma unroll
-    for (int k = 0; k < MAXPER; ++k) {
-        const int b = b0 + k;
-        const bool in = k < per && b < B;
-        len[k] = in ? a.len[b] : 0;
-        nn[k] = in ? a.n_new[b] : 0;
+    for (int k = 0; k < PER; ++k) {
+        len[k] = b0 + k < B ? a.len[b0 + k] : 0;
+        nn[k] = b0 + k < B ? a.n_new[b0 + k] : 0;
     }
+    int64_t tokens = 0, tokens_all;
+    uint32_t back = 0, back_all, used[PER];
+    bool sane[PER], finished = false;
 #pragma unroll
-    for (int k = 0; k < MAXPER; ++k) {
+    for (int k = 0; k < PER; ++k) {
         tokens += nn[k] > 0 ? nn[k] : 0;
-        const bool sane = len[k] >= 0 && len[k] <= room;
-        back += nn[k] == -1 && sane ? (len[k] + P - 1) / P : 0;
-    }
-    const int64_t tokens_upto = block_scan(tokens, s_part);
-    const int64_t back_upto = block_scan(back, s_part);
-    const int64_t count = s_free;
-    const bool stack_ok = count >= 0 && count <= a.n_stack;
-    const int64_t space = stack_ok ? a.n_stack - count : -1;  // places left on the stack
-
-    // which requests fit, whose pages come back, and what is needed
-    int64_t cu = tokens_upto - tokens, bk = back_upto - back, need = 0, kept = 0;
-    int64_t want[MAXPER];
-    int32_t state[MAXPER];
-#pragma unroll
-    for (int k = 0; k < MAXPER; ++k) {
-        const int b = b0 + k;
-        want[k] = 0;
-        state[k] = SA_PAGED_REFUSED;
-        if (!(k < per && b < B)) continue;
-        const bool sane = len[k] >= 0 && len[k] <= room;
-        const int64_t used = sane ? (len[k] + P - 1) / P : 0, n = nn[k] > 0 ? nn[k] : 0;
-        cu += n;
-        if (rank == 0) a.cu_new[b + 1] = cu;
-        s_end[b] = (int32_t)(cu < a.capacity ? cu : a.capacity);
-        s_len[b] = sane ? (int32_t)len[k] : 0;
-        s_new[b] = kRefused;
+        sane[k] = len[k] >= 0 && len[k] <= room;
+        used[k] = sane[k] ? pages(len[k]) : 0;
         if (nn[k] == -1) {
-            bk += used;
-            if (sane && (bk <= space || (used == 0 && stack_ok))) {
-                state[k] = SA_PAGED_OK;
-                kept += used;
-            }
-        } else if (nn[k] >= 0 && sane && len[k] + n <= room && cu <= a.capacity) {
-            state[k] = SA_PAGED_NO_PAGES;  // until its pages are known to be there
-            want[k] = (len[k] + n + P - 1) / P - used;
-            need += want[k];
+            back = add_sat(back, used[k]);
+            finished = true;
         }
     }
-    const int64_t need_upto = block_scan(need, s_part);
-    const int64_t kept_upto = block_scan(kept, s_part);
-    __syncthreads();
-    const int64_t kept_all = s_part[kWarps - 1];
-    const int64_t top = stack_ok ? count + kept_all : 0;
-    int64_t upto = need_upto - need, place = count + kept_upto - kept, taken = 0;
+    if (tid == 0) s_taken = 0;
+    int64_t cu = tokens;
+    uint32_t bk = back;
+    finished = block_scan<NW>(cu, bk, tokens_all, back_all, finished, s_x, s_y);
+    const bool stack_ok = count >= 0 && count <= a.n_stack;
+    const uint32_t space = stack_ok ? (uint32_t)(a.n_stack - count) : 0;  // places left
+    cu -= tokens;
+    // (a saturated sum is above every space, and so are the sums before it here)
+    bk = bk == 0xffffffffu ? bk : bk - back;
+
+    // which requests fit, whose pages come back, and what is needed
+    uint32_t need = 0, kept = 0, want[PER];
+    int32_t state[PER];
+    {
+        int64_t c = cu;
+        uint32_t b = bk;
 #pragma unroll
-    for (int k = 0; k < MAXPER; ++k) {
+        for (int k = 0; k < PER; ++k) {
+            want[k] = 0;
+            state[k] = SA_PAGED_REFUSED;
+            if (b0 + k >= B) continue;
+            const int64_t n = nn[k] > 0 ? nn[k] : 0;
+            c += n;
+            if (nn[k] == -1) {
+                b = add_sat(b, used[k]);
+                if (sane[k] && stack_ok && (b <= space || used[k] == 0)) {
+                    state[k] = SA_PAGED_OK;
+                    kept += used[k];
+                }
+            } else if (nn[k] >= 0 && sane[k] && len[k] + n <= room && c <= a.capacity) {
+                state[k] = SA_PAGED_NO_PAGES;  // until its pages are known to be there
+                want[k] = pages(len[k] + n) - used[k];
+                need += want[k];
+            }
+        }
+    }
+    uint32_t need_upto = need, kept_upto = kept, need_all, kept_all;
+    block_scan<NW>(need_upto, kept_upto, need_all, kept_all, false, s_z, s_w);
+    const uint32_t top = stack_ok ? (uint32_t)count + kept_all : 0;
+    uint32_t upto = need_upto - need, place = (uint32_t)count + kept_upto - kept, taken = 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
         const int b = b0 + k;
-        if (!(k < per && b < B)) continue;
-        const int64_t used = (int64_t)(s_len[b] + P - 1) / P;
+        if (b >= B) continue;
+        int32_t first = kRefused;
         if (nn[k] == -1) {
-            // (s_new of a finished request: where its pages go on the stack)
             if (state[k] == SA_PAGED_OK) {
-                s_new[b] = (int32_t)place;
-                place += used;
+                first = (int32_t)place;
+                place += used[k];
             }
         } else if (state[k] == SA_PAGED_NO_PAGES) {
             upto += want[k];
             if (want[k] == 0 || upto <= top) {
                 state[k] = SA_PAGED_OK;
-                s_new[b] = want[k] ? (int32_t)(upto - want[k]) : 0;
-                taken += want[k];
+                first = want[k] ? (int32_t)(upto - want[k]) : 0;
+                if (want[k]) taken = upto;  // (sums only grow: the last is the largest)
             }
         }
+        cu += nn[k] > 0 ? nn[k] : 0;
+        if (rank == 0) a.cu_new[b + 1] = cu;
+        s_end[b] = (int32_t)(cu < a.capacity ? cu : a.capacity);
+        s_len[b] = !sane[k] ? 0 : nn[k] == -1 ? -1 - (int32_t)len[k] : (int32_t)len[k];
+        s_new[b] = first;
     }
-    const int64_t taken_upto = block_scan(taken, s_part);  // also: shared arrays are complete
+    if (taken) atomicMax(&s_taken, taken);
     if (rank == 0 && tid == 0) a.cu_new[0] = 0;
+    __syncthreads();
 
     // returned pages go on the stack: a warp per finished request
-    const int warp = rank * kWarps + (tid >> 5), nwarp = ncta * kWarps, lane = tid & 31;
-    for (int b = warp; b < B; b += nwarp) {
-        if (a.n_new[b] != -1 || s_new[b] == kRefused) continue;
-        const int64_t used = (int64_t)(s_len[b] + P - 1) / P;
-        for (int64_t p = lane; p < used; p += 32)
-            a.free_pages[s_new[b] + p] = a.block_table[(int64_t)b * a.max_pages + p];
+    if (finished) {
+        const int warp = rank * NW + (tid >> 5), lane = tid & 31;
+        for (int b = warp; b < B; b += ncta * NW) {
+            if (s_len[b] >= 0 || s_new[b] == kRefused) continue;
+            const int32_t n = (int32_t)pages(-1 - s_len[b]);
+            const int32_t *from = a.block_table + (int64_t)b * a.max_pages;
+            int32_t *to = a.free_pages + s_new[b];
+            for (int32_t p = lane; p < n; p += 128) {
+                int32_t x[4];
+#pragma unroll
+                for (int y = 0; y < 4; ++y) x[y] = p + 32 * y < n ? from[p + 32 * y] : 0;
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                    if (p + 32 * y < n) to[p + 32 * y] = x[y];
+            }
+        }
     }
-    cluster.sync();
+    if (ncta > 1) cluster.sync();
+    else if (finished) __syncthreads();
 
     // new state (every CTA has read the old one)
+    if (rank == 0) {
 #pragma unroll
-    for (int k = 0; k < MAXPER; ++k) {
-        const int b = b0 + k;
-        if (rank != 0 || !(k < per && b < B)) continue;
-        a.status[b] = state[k];
-        a.len_out[b] = state[k] != SA_PAGED_OK ? len[k]
-                       : nn[k] == -1           ? 0
-                                               : len[k] + nn[k];
-    }
-    if (rank == 0 && tid == kThreads - 1) *a.free_count_out = stack_ok ? top - taken_upto : count;
-
-    // tokens: a run of kRun consecutive ones per thread, the request of the
-    // first found by bisection
-    constexpr int kRun = 4;
-    const int64_t step = (int64_t)ncta * kThreads * kRun;
-    for (int64_t t0 = ((int64_t)rank * kThreads + tid) * kRun; t0 < a.capacity; t0 += step) {
-        int lo = 0, hi = B;  // first request whose tokens end after t0
-        while (lo < hi) {
-            const int mid = (lo + hi) >> 1;
-            if (s_end[mid] > t0) hi = mid;
-            else lo = mid + 1;
+        for (int k = 0; k < PER; ++k) {
+            const int b = b0 + k;
+            if (b >= B) continue;
+            a.status[b] = state[k];
+            a.len_out[b] = state[k] != SA_PAGED_OK ? len[k] : nn[k] == -1 ? 0 : len[k] + nn[k];
         }
-        int b = lo;
+        if (tid == 0) *a.free_count_out = stack_ok ? (int64_t)(top - s_taken) : count;
+    }
+
+    // tokens: kRun of a thread, NT apart, so that their loads overlap and
+    // neighbours store together
+    constexpr int kRun = 4;
+    const int32_t capacity = (int32_t)a.capacity;
+    for (int64_t t0 = (int64_t)rank * NT * kRun; t0 < capacity; t0 += (int64_t)ncta * NT * kRun) {
+        int32_t page[kRun], row[kRun], pos[kRun];
+        uint32_t off[kRun];
+        int32_t *entry[kRun];
+        int32_t lo[kRun], hi[kRun];
+#pragma unroll
+        for (int x = 0; x < kRun; ++x) lo[x] = 0, hi[x] = B;
+        // first request whose tokens end after the token
+        for (int n = B; n; n >>= 1) {
+#pragma unroll
+            for (int x = 0; x < kRun; ++x) {
+                const int mid = (lo[x] + hi[x]) >> 1;
+                if (lo[x] < hi[x]) {
+                    if (s_end[mid] > t0 + x * NT + tid) hi[x] = mid;
+                    else lo[x] = mid + 1;
+                }
+            }
+        }
 #pragma unroll
         for (int x = 0; x < kRun; ++x) {
-            const int64_t t = t0 + x;
-            if (t >= a.capacity) break;
-            while (b < B && s_end[b] <= t) ++b;
-            int64_t slot = -1, pos = -1;
-            int32_t row = -1;
-            if (b < B && s_new[b] != kRefused) {
+            const int64_t t = t0 + x * NT + tid;
+            const int b = lo[x];
+            row[x] = pos[x] = page[x] = -1;
+            off[x] = 0;
+            entry[x] = nullptr;
+            if (t < capacity && b < B && s_new[b] != kRefused) {
                 const int32_t L = s_len[b];
-                const int64_t first = b ? s_end[b - 1] : 0;
-                const int64_t used = ((int64_t)L + P - 1) / P;
-                pos = L + (t - first);
-                row = b;
-                const int64_t p = pos / P, off = pos - p * P;
-                int32_t *entry = a.block_table + (int64_t)b * a.max_pages + p;
-                int32_t page;
-                if (p < used) {
-                    page = *entry;
+                row[x] = b;
+                pos[x] = L + (int32_t)(t - (b ? s_end[b - 1] : 0));
+                const uint32_t p = divide((uint32_t)pos[x], args.page), u = pages(L);
+                off[x] = (uint32_t)pos[x] - p * P;
+                int32_t *e = a.block_table + (int64_t)b * a.max_pages + p;
+                if (p < u) {
+                    page[x] = *e;
                 } else {
-                    page = __ldcg(a.free_pages + (top - 1 - (s_new[b] + (p - used))));
-                    if (off == 0) *entry = page;
+                    page[x] = __ldcg(a.free_pages + (top - 1 - ((uint32_t)s_new[b] + (p - u))));
+                    if (off[x] == 0) entry[x] = e;
                 }
-                slot = page >= 0 ? (int64_t)page * P + off : -1;
             }
-            a.slot[t] = slot;
-            a.pos[t] = pos;
-            a.row[t] = row;
+        }
+#pragma unroll
+        for (int x = 0; x < kRun; ++x) {
+            const int64_t t = t0 + x * NT + tid;
+            if (t >= capacity) continue;
+            if (entry[x]) *entry[x] = page[x];
+            a.slot[t] = page[x] >= 0 ? (int64_t)page[x] * P + off[x] : -1;
+            a.pos[t] = pos[x];
+            a.row[t] = row[x];
         }
     }
 }
 
-template <int MAXPER>
-sa_status launch_plan(const sa_paged_step &p, cudaStream_t s) {
-    const void *fn = (const void *)paged_plan_kernel<MAXPER>;
-    const int smem = 3 * 4 * (int)p.B;
+template <int NT, int PER>
+sa_status launch_plan(const PlanArgs &p, cudaStream_t s) {
+    const void *fn = (const void *)paged_plan_kernel<NT, PER>;
     // the opt-in holds for the largest B of this variant
-    const int most = 3 * 4 * MAXPER * kThreads;
-    SA_CUDA_TRY(sa_smem_optin(fn, most));
+    SA_CUDA_TRY(sa_smem_optin(fn, 3 * 4 * PER * NT));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
-    const int ncta = p.capacity > 2 * kThreads ? 8 : 1;
+    const int ncta = p.s.capacity > 2048 ? 8 : 1;
     cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = 3 * 4 * (size_t)p.s.B;
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ncta;
@@ -241,14 +293,18 @@ sa_status launch_plan(const sa_paged_step &p, cudaStream_t s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
-    SA_LAUNCH("paged_plan", s, e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<MAXPER>, p));
+    SA_LAUNCH("paged_plan", s, e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<NT, PER>, p));
     SA_CUDA_TRY(e);
     return SA_OK;
 }
 
 }  // namespace
 
-sa_status sa_paged_plan(const sa_paged_step &p, cudaStream_t s) {
-    static_assert(SA_PAGED_MAX_REQUESTS <= 8 * kThreads, "requests per thread");
-    return p.B <= kThreads ? launch_plan<1>(p, s) : launch_plan<8>(p, s);
+sa_status sa_paged_plan(const sa_paged_step &step, cudaStream_t s) {
+    const PlanArgs p = {step, make_divide((uint32_t)step.page_size)};
+    static_assert(SA_PAGED_MAX_REQUESTS <= 8 * 1024, "requests per thread");
+    if (p.s.B <= 256 && p.s.capacity <= 2048) return launch_plan<256, 1>(p, s);
+    if (p.s.B <= 1024) return launch_plan<1024, 1>(p, s);
+    if (p.s.B <= 2048) return launch_plan<1024, 2>(p, s);
+    return launch_plan<1024, 8>(p, s);
 }
