@@ -248,7 +248,7 @@ typedef enum {
  * block_table other than newly taken pages, and of free_pages other than
  * returned ones, stay as they were.  A free_count outside [0, n_stack] means
  * that no page is taken or returned.  1 <= B <= SA_PAGED_MAX_REQUESTS;
- * capacity and n_stack >= 1 and < 2^31. */
+ * 1 <= capacity <= 2^30; 1 <= n_stack < 2^31. */
 #define SA_PAGED_MAX_REQUESTS 8192
 typedef struct {
     int64_t B, max_pages, page_size, capacity, n_stack;

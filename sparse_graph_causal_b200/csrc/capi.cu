@@ -599,7 +599,7 @@ sa_status sparse_attn_paged_plan(const sa_paged_step *p, void *stream) {
     const void *narrow[] = {p->n_new, p->block_table, p->free_pages, p->row, p->status};
     for (const void *a : narrow)
         if (!array_ok(a, 4)) return SA_ERR_INVALID_ARG;
-    if (p->B > SA_PAGED_MAX_REQUESTS || p->capacity > kInt32Max || p->n_stack > kInt32Max ||
+    if (p->B > SA_PAGED_MAX_REQUESTS || p->capacity > 1 << 30 || p->n_stack > kInt32Max ||
         p->page_size > kInt32Max || p->max_pages > kInt32Max / p->page_size)
         return SA_ERR_UNSUPPORTED;
     return sa_paged_plan(*p, as_stream(stream));

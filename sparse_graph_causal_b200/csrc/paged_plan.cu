@@ -71,6 +71,7 @@ __device__ __forceinline__ bool block_scan(A &x, uint32_t &y, A &x_all, uint32_t
 struct PlanArgs {
     sa_paged_step s;
     Divide page;
+    int32_t size;  // power of two above B
 };
 
 // First new page of a request counted from the top of the stack (a finished
@@ -88,7 +89,9 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
     const int B = (int)a.B, tid = threadIdx.x;
     // the end of each request's tokens (clipped to capacity), its length (-1 -
     // length if it is finished) and its first new page
-    int32_t *s_end = smem, *s_len = smem + B, *s_new = smem + 2 * B;
+    // (s_end: a power of two above B of entries, the rest never reached)
+    const int a_size = args.size;
+    int32_t *s_end = smem, *s_len = smem + a_size, *s_new = s_len + B;
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = (int)cluster.block_rank(), ncta = (int)cluster.num_blocks();
     const int64_t room = a.max_pages * a.page_size;
@@ -119,6 +122,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
         }
     }
     if (tid == 0) s_taken = 0;
+    for (int b = B + tid; b < a_size; b += NT) s_end[b] = 0x7fffffff;
     int64_t cu = tokens;
     uint32_t bk = back;
     finished = block_scan<NW>(cu, bk, tokens_all, back_all, finished, s_x, s_y);
@@ -223,27 +227,20 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
     // neighbours store together
     constexpr int kRun = 4;
     const int32_t capacity = (int32_t)a.capacity;
-    for (int64_t t0 = (int64_t)rank * NT * kRun; t0 < capacity; t0 += (int64_t)ncta * NT * kRun) {
+    for (int32_t t0 = rank * NT * kRun; t0 < capacity; t0 += ncta * NT * kRun) {
         int32_t page[kRun], row[kRun], pos[kRun];
         uint32_t off[kRun];
         int32_t *entry[kRun];
-        int32_t lo[kRun], hi[kRun];
+        // requests whose tokens end before the token (without branches: four
+        // searches side by side)
+        int32_t lo[kRun] = {};
+        for (int n = a_size >> 1; n; n >>= 1)
 #pragma unroll
-        for (int x = 0; x < kRun; ++x) lo[x] = 0, hi[x] = B;
-        // first request whose tokens end after the token
-        for (int n = B; n; n >>= 1) {
-#pragma unroll
-            for (int x = 0; x < kRun; ++x) {
-                const int mid = (lo[x] + hi[x]) >> 1;
-                if (lo[x] < hi[x]) {
-                    if (s_end[mid] > t0 + x * NT + tid) hi[x] = mid;
-                    else lo[x] = mid + 1;
-                }
-            }
-        }
+            for (int x = 0; x < kRun; ++x)
+                lo[x] += s_end[lo[x] + n - 1] <= t0 + x * NT + tid ? n : 0;
 #pragma unroll
         for (int x = 0; x < kRun; ++x) {
-            const int64_t t = t0 + x * NT + tid;
+            const int32_t t = t0 + x * NT + tid;
             const int b = lo[x];
             row[x] = pos[x] = page[x] = -1;
             off[x] = 0;
@@ -265,7 +262,7 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
         }
 #pragma unroll
         for (int x = 0; x < kRun; ++x) {
-            const int64_t t = t0 + x * NT + tid;
+            const int32_t t = t0 + x * NT + tid;
             if (t >= capacity) continue;
             if (entry[x]) *entry[x] = page[x];
             a.slot[t] = page[x] >= 0 ? (int64_t)page[x] * P + off[x] : -1;
@@ -279,13 +276,13 @@ template <int NT, int PER>
 sa_status launch_plan(const PlanArgs &p, cudaStream_t s) {
     const void *fn = (const void *)paged_plan_kernel<NT, PER>;
     // the opt-in holds for the largest B of this variant
-    SA_CUDA_TRY(sa_smem_optin(fn, 3 * 4 * PER * NT));
+    SA_CUDA_TRY(sa_smem_optin(fn, 4 * 4 * PER * NT));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     const int ncta = p.s.capacity > 2048 ? 8 : 1;
     cfg.gridDim = dim3(ncta);
     cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = 3 * 4 * (size_t)p.s.B;
+    cfg.dynamicSmemBytes = 4 * (size_t)(p.size + 2 * p.s.B);
     cfg.stream = s;
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = ncta;
@@ -301,10 +298,11 @@ sa_status launch_plan(const PlanArgs &p, cudaStream_t s) {
 }  // namespace
 
 sa_status sa_paged_plan(const sa_paged_step &step, cudaStream_t s) {
-    const PlanArgs p = {step, make_divide((uint32_t)step.page_size)};
+    PlanArgs p = {step, make_divide((uint32_t)step.page_size), 1};
+    while (p.size <= step.B) p.size *= 2;
     static_assert(SA_PAGED_MAX_REQUESTS <= 8 * 1024, "requests per thread");
     if (p.s.B <= 256 && p.s.capacity <= 2048) return launch_plan<256, 1>(p, s);
     if (p.s.B <= 1024) return launch_plan<1024, 1>(p, s);
     if (p.s.B <= 2048) return launch_plan<1024, 2>(p, s);
-    return launch_plan<1024, 8>(p, s);
+    return p.s.B <= 4096 ? launch_plan<1024, 4>(p, s) : launch_plan<1024, 8>(p, s);
 }

@@ -36,7 +36,7 @@ def _step(sa, **change):
 @pytest.mark.parametrize("change, status", [
     (dict(B=0), INVALID), (dict(B=8193), UNSUPPORTED), (dict(max_pages=0), INVALID),
     (dict(page_size=0), INVALID), (dict(capacity=0), INVALID), (dict(n_stack=0), INVALID),
-    (dict(capacity=1 << 31), UNSUPPORTED), (dict(n_stack=1 << 31), UNSUPPORTED),
+    (dict(capacity=1 << 31), UNSUPPORTED), (dict(capacity=(1 << 30) + 1), UNSUPPORTED), (dict(n_stack=1 << 31), UNSUPPORTED),
     (dict(max_pages=1 << 30, page_size=2), UNSUPPORTED),
     (dict(max_pages=1, page_size=1 << 31), UNSUPPORTED),
     (dict(len=None), INVALID), (dict(n_new=None), INVALID), (dict(block_table=None), INVALID),
@@ -70,7 +70,7 @@ BAD_CACHES = [
     (dict(D=96), UNSUPPORTED), (dict(k_scale=A), INVALID), (dict(v_scale=A), INVALID),
     (dict(dtype=2), INVALID), (dict(dtype=2, k_scale=A), INVALID),
     (dict(dtype=2, k_scale=A + 2, v_scale=A), INVALID),
-    (dict(n_pages=1 << 31), UNSUPPORTED), (dict(page_size=1 << 31), UNSUPPORTED),
+    (dict(n_pages=1 << 31), UNSUPPORTED), (dict(Hkv=(1 << 24) + 1), UNSUPPORTED), (dict(page_size=1 << 31), UNSUPPORTED),
 ]
 
 
@@ -130,6 +130,7 @@ def test_decode_refusals(sa):
               dict(scale=float("nan")), dict(scale=float("inf")), dict(lse=None), dict(lse=A + 4)):
         assert call(**x) == INVALID, x
     assert call(M=1 << 27) == UNSUPPORTED        # 2^27 pages of 16 rows
+    assert call(M=(1 << 26) + 1) == UNSUPPORTED  # more than 2^30 positions
     assert call(rows=1 << 31) == UNSUPPORTED
 
 
