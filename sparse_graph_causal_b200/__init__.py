@@ -346,7 +346,8 @@ def _call_on(index: int, stream, where: str, fn, *args):
     """fn(*args, stream) with the tensors' device current (the library launches
     on the current one), on its current stream unless one is given."""
     if index == torch._C._cuda_getDevice():
-        status = fn(*args, _stream(stream))
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
+                    else _stream(stream))
     else:
         with torch.cuda.device(index):
             status = fn(*args, _stream(stream))

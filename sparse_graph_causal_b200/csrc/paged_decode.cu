@@ -526,12 +526,13 @@ struct MmaTile {
 
 // ------------------------------------------------------------ fp32 tiles
 
-template <int kD, int NB>
+template <int kD, int kNQ>
 struct FmaTile {
     using Out = float;
-    static constexpr int D = kD, NQ = 8 * NB, RB = 4 * D;
+    static constexpr int D = kD, NQ = kNQ, RB = 4 * D;
     static constexpr int KT = 1024 / D;   // 8 KB of keys and values
-    static constexpr int kStages = D == 128 || NB == 2 ? 2 : 3, kWarps = 8, kOcc = 1;
+    static constexpr int kStages = NQ == 16 || (NQ == 8 && D == 128) ? 2 : 3;
+    static constexpr int kWarps = 8, kOcc = 1;
     static constexpr int kStageBytes = 2 * KT * RB;
     static constexpr int kOwnBytes = NQ * D * 4 + NQ * KT * 4;  // queries and probabilities
     static constexpr int C = D / 4;       // 16-byte pieces of a row
@@ -679,11 +680,22 @@ struct Layout {
     static_assert(kBytes * Tile::kWarps * Tile::kOcc <= 227 * 1024 - 4096 * Tile::kOcc, "smem");
 };
 
+// Query heads of block u of a token: first head and how many.
+struct Block {
+    int64_t kvh;
+    int32_t first, gq;
+};
+template <int NQ>
+__device__ __forceinline__ Block block_of(const DecodeArgs &a, int32_t u) {
+    const int32_t kvh = u / a.QB, q0 = (u - kvh * a.QB) * NQ;
+    return {kvh, kvh * a.G + q0, min(NQ, a.G - q0)};
+}
+
 // Edges [x0, x1) of a token's row for one block of query heads.
 template <typename Tile>
 __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const GraphView &g,
-                                          const Token &t, int64_t kvh, int32_t x0, int32_t x1,
-                                          uint8_t *mem) {
+                                          const Token &t, int64_t token, const Block &b, int32_t x0,
+                                          int32_t x1, uint8_t *mem) {
     using M = Layout<Tile>;
     constexpr int S = Tile::kStages, KT = Tile::KT;
     const int lane = threadIdx.x & 31;
@@ -719,7 +731,7 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
         __syncwarp();
         if (lane < KT)
             rows[lane] =
-                ok ? (((int64_t)page * a.Hkv + kvh) * a.page.by + off) * Tile::RB : -1;
+                ok ? (((int64_t)page * a.Hkv + b.kvh) * a.page.by + off) * Tile::RB : -1;
         if (lane == 0) masks[stage] = mask;
         __syncwarp();
         tile.copy(a, mem + stage * Tile::kStageBytes, rows, mask == all);
@@ -737,6 +749,7 @@ __device__ __forceinline__ void run_edges(Tile &tile, const DecodeArgs &a, const
         }
         copies_commit();
     }
+    tile.begin(a, mem + M::kRing, token, b.first, b.gq);  // with the first copies under way
     // (the copies of a later tile come after the work on this one: in front they
     // would hold up its loads from shared memory)
     for (int32_t i = 0; i < n; ++i) {
@@ -801,17 +814,6 @@ __device__ __noinline__ void merge_parts(int tid, int threads, const float *cons
     }
 }
 
-// Query heads of block u of a token: first head and how many.
-struct Block {
-    int64_t kvh;
-    int32_t first, gq;
-};
-template <int NQ>
-__device__ __forceinline__ Block block_of(const DecodeArgs &a, int32_t u) {
-    const int32_t kvh = u / a.QB, q0 = (u - kvh * a.QB) * NQ;
-    return {kvh, kvh * a.G + q0, min(NQ, a.G - q0)};
-}
-
 // The direct way: CTA b has block b mod U of token b / U.
 template <typename Tile>
 __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
@@ -829,8 +831,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     const int32_t x1 = min(t.deg, (int32_t)((int64_t)tiles * (warp + 1) / nw) * Tile::KT);
     uint8_t *own = mem + warp * M::kBytes;
     Tile tile;
-    tile.begin(a, own + M::kRing, n, b.first, b.gq);
-    run_edges(tile, a, g, t, b.kvh, x0, x1, own);
+    run_edges(tile, a, g, t, n, b, x0, x1, own);
     write_part(tile, (float *)own);
     if ((threadIdx.x & 31) == 0) s_part[2 * warp] = (float *)own;
     __syncthreads();
@@ -910,12 +911,9 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     if (x < x_end) {
         // the row of tile x
         const int64_t y = quotient(x, U);
-        int lo = 0, hi = NT - 1;  // last run that begins at or before y
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (s_start[mid] <= y) lo = mid;
-            else hi = mid - 1;
-        }
+        int lo = -1;  // last run that begins at or before y
+#pragma unroll
+        for (int i = 0; i < NW; ++i) lo += __popc(__ballot_sync(kFull, s_start[32 * i + lane] <= y));
         int64_t n = lo * per, before = s_start[lo];
         if (per > 1) {
             for (;; n += 32) {
@@ -951,8 +949,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
             if (tile1 > 0) {
                 if (t.bad && lane == 0) atomicOr(a.err, SA_DEVERR_BOUNDS);
                 const Block b = block_of<Tile::NQ>(a, u);
-                tile.begin(a, own + M::kRing, n, b.first, b.gq);
-                run_edges(tile, a, g, t, b.kvh, tile0 * KT, min(t.deg, tile1 * KT), own);
+                run_edges(tile, a, g, t, n, b, tile0 * KT, min(t.deg, tile1 * KT), own);
                 const bool goes_on = tile0 > 0, ends = tile1 == tiles;
                 // (the ring is free, but not for long if more rows follow)
                 const bool whole = !goes_on && ends, stays = x + (to - from) >= x_end;
@@ -1088,7 +1085,9 @@ auto with_tile(const sa_paged_cache &c, int64_t G, F f)
                          : f((MmaTile<__nv_bfloat16, d, 1> *)0);                      \
         if (c.dtype == SA_E4M3)                                                       \
             return G > 8 ? f((MmaTile<E4m3, d, 2> *)0) : f((MmaTile<E4m3, d, 1> *)0); \
-        return G > 8 ? f((FmaTile<d, 2> *)0) : f((FmaTile<d, 1> *)0);                 \
+        return G > 8   ? f((FmaTile<d, 16> *)0)                                       \
+               : G > 4 ? f((FmaTile<d, 8> *)0)                                        \
+                       : f((FmaTile<d, 4> *)0);                                       \
     }
     SA_PAGED_TILE(32)
     SA_PAGED_TILE(64)
@@ -1122,13 +1121,19 @@ sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, bool
     if (direct) {
         const int64_t blocks = a.N * a.Hkv * a.QB;
         if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
-        int nw = (int)((longest + Tile::KT - 1) / Tile::KT);
+        // a warp for each tile, but no more warps than the GPU holds: with many
+        // rows, several CTAs of few warps overlap one's start with another's work
+        int sms = 0;
+        SA_CUDA_TRY(sa_sm_count(&sms));
+        const int64_t held = (int64_t)Tile::kWarps * Tile::kOcc * sms;
+        int64_t nw = (longest + Tile::KT - 1) / Tile::KT;
+        if (nw > (held + blocks - 1) / blocks) nw = (held + blocks - 1) / blocks;
         nw = nw < 1 ? 1 : nw > Tile::kWarps ? Tile::kWarps : nw;
         SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_direct<Tile>,
                                   Tile::kWarps * M::kBytes));
         SA_LAUNCH("paged_decode", s,
                   paged_decode_direct<Tile>
-                  <<<(unsigned)blocks, 32 * nw, nw * M::kBytes, s>>>(a, g));
+                  <<<(unsigned)blocks, 32 * (int)nw, (int)nw * M::kBytes, s>>>(a, g));
         SA_CUDA_TRY(cudaGetLastError());
         return SA_OK;
     }
