@@ -165,7 +165,7 @@ struct DecodeArgs {
     void *out;
     float *lse;
     float *warp_part, *cta_part;  // partial rows: slots [warp], [CTA][2]
-    int4 *cut;                    // per CTA: the row that starts there and is cut
+    int4 *cut;  // per CTA: first query head, last CTA and queries of the row that goes on
     int *err;
 };
 
@@ -855,6 +855,14 @@ struct Shares {
 // What the start of a row costs a warp (positions, pages and the first copies
 // one after the other, then the merge), in tiles.  The shares count it.
 constexpr int kRowStart = 3;
+// A cut row's parts in a CTA: the row's first query head, entry of the first part
+// and number of parts, queries, the row's last CTA, whether it starts and ends here.
+struct Cut {
+    int64_t nh;
+    int first, count, gq, last;
+    bool starts, ends;
+};
+
 // Fewest tiles worth a warp: below, a share is mostly its own start and merge.
 constexpr int kLeastTiles = 4;
 
@@ -868,12 +876,11 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     extern __shared__ __align__(128) uint8_t mem[];
     __shared__ int64_t s_start[NT + 1];  // row tiles before each thread's rows
     __shared__ int64_t s_sum[NW];
-    __shared__ int64_t s_unit[NW][2];    // the cut rows of each warp: one it goes on with, one
-    __shared__ int64_t s_end[NW];        //   it starts; the end of the latter
-    __shared__ int s_ends[NW];           // the former ends here
-    __shared__ const float *s_part[2 * NW + 2 * NW];  // their parts; then each warp's ring
-    __shared__ int s_group[2 * NW];      // rows cut in this CTA: first part, how many
-    __shared__ int s_groups;
+    // parts of cut rows: of the row that each warp goes on with and of the one that it
+    // starts; then each warp's ring
+    __shared__ const float *s_part[4 * NW];
+    // cut rows with parts in this CTA: the one it goes on with, those its warps start
+    __shared__ Cut s_cut[1 + NW];
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t U = (int64_t)a.Hkv * a.QB;
@@ -893,7 +900,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
             if (lane >= o) x += y;
         }
         if (lane == 31) s_sum[warp] = x;
-        if (lane < 2) s_unit[warp][lane] = -1;
+        if (tid <= NW) s_cut[tid].count = 0;
         __syncthreads();
         for (int w = 0; w < warp; ++w) x += s_sum[w];
         s_start[tid + 1] = x;
@@ -963,12 +970,17 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
                                                   (Out *)a.out + nh * D, a.lse + nh);
                     __syncwarp();
                 } else {
-                    const int which = goes_on ? 0 : 1;
+                    const int entry = 2 * warp + (goes_on ? 0 : 1);
                     if (lane == 0) {
-                        s_part[2 * warp + which] = part;
-                        s_unit[warp][which] = n * U + u;
-                        if (goes_on) s_ends[warp] = ends;
-                        else s_end[warp] = x + (tiles + kRowStart - from);
+                        s_part[entry] = part;
+                        if (!goes_on || warp == 0) {
+                            // the CTA's first part: it knows how far the row reaches
+                            const int64_t end = shares.of(x - from + tiles + kRowStart - 1);
+                            const int64_t here = min(end, W - warp + nw - 1);
+                            s_cut[goes_on ? 0 : 1 + warp] =
+                                Cut{n * a.H + b.first, entry, (int)(here - W) + 1, b.gq,
+                                    (int)quotient(end, nw), !goes_on, here == end};
+                        }
                     }
                 }
             }
@@ -984,39 +996,19 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     }
     __syncthreads();
 
-    // the CTA's cut rows, in order: parts of one row are neighbours
-    if (warp == 0) {
-        const int64_t unit = lane < 2 * NW ? s_unit[lane >> 1][lane & 1] : -1;
-        const unsigned there = __ballot_sync(kFull, unit >= 0);
-        const unsigned below = there & ((1u << lane) - 1);
-        const int64_t before = __shfl_sync(kFull, unit, below ? 31 - __clz(below) : lane);
-        const bool first = unit >= 0 && (!below || before != unit);
-        const unsigned firsts = __ballot_sync(kFull, first);
-        const unsigned after = firsts & ~((2u << lane) - 1);
-        const unsigned upto = after ? (1u << (__ffs(after) - 1)) - 1 : kFull;
-        if (first)
-            s_group[__popc(firsts & ((1u << lane) - 1))] =
-                lane | __popc(there & upto & ~((1u << lane) - 1)) << 8;
-        if (lane == 0) s_groups = __popc(firsts);
-    }
-    __syncthreads();
+    // each row's parts in this CTA become one, or the output
     int4 cut = make_int4(-1, -1, 0, 0);
-    for (int i = 0; i < s_groups; ++i) {
-        const int first = s_group[i] & 255, count = s_group[i] >> 8, w0 = first >> 1;
-        const bool starts = first & 1;
-        // (a part of its own start alone goes on elsewhere)
-        const int last = w0 + count - 1;
-        const bool ends = (!starts || count > 1) && s_ends[last];
-        const int64_t unit = s_unit[w0][first & 1], n = quotient(unit, U);
-        const Block b = block_of<Tile::NQ>(a, (int32_t)(unit - n * U));
-        float *to = starts && ends ? nullptr
-                                   : a.cta_part + ((int64_t)blockIdx.x * 2 + (starts ? 1 : 0)) * PF;
-        const int64_t nh = n * a.H + b.first;
-        merge_parts<Out, Tile::NQ, D>(tid, NT, s_part, first, count, b.gq, to, (Out *)a.out + nh * D,
-                                      a.lse + nh);
-        if (starts && !ends)
-            cut = make_int4((int)(unit & 0xffffffff), (int)(unit >> 32),
-                            (int)quotient(shares.of(s_end[w0] - 1), nw), 0);
+#pragma unroll 1
+    for (int i = 0; i <= NW; ++i) {
+        const Cut c = s_cut[i];
+        if (c.count == 0) continue;
+        float *to = c.starts && c.ends
+                        ? nullptr
+                        : a.cta_part + ((int64_t)blockIdx.x * 2 + (c.starts ? 1 : 0)) * PF;
+        merge_parts<Out, Tile::NQ, D>(tid, NT, s_part, c.first, c.count, c.gq, to,
+                                      (Out *)a.out + c.nh * D, a.lse + c.nh);
+        if (c.starts && !c.ends)
+            cut = make_int4((int)c.nh, (int)(c.nh >> 32), c.last, c.gq);
     }
     if (tid == 0) a.cut[blockIdx.x] = cut;
 }
@@ -1033,12 +1025,9 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) 
     __shared__ float4 s_o[R][C];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int4 cut = __ldcg(a.cut + blockIdx.x);
-    const int64_t unit = (int64_t)(uint32_t)cut.x | ((int64_t)cut.y << 32);
-    if (unit < 0) return;
-    const int64_t U = (int64_t)a.Hkv * a.QB, n = quotient(unit, U);
-    const Block b = block_of<NQ>(a, (int32_t)(unit - n * U));
     const int q = blockIdx.y, c = threadIdx.x % C, r = threadIdx.x / C;
-    if (q >= b.gq) return;
+    if (q >= cut.w) return;
+    const int64_t nh = ((int64_t)(uint32_t)cut.x | ((int64_t)cut.y << 32)) + q;
     const int count = cut.z - (int)blockIdx.x + 1;
     State s;
 #pragma unroll 4
@@ -1053,25 +1042,36 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) 
     if (r != 0) return;
 #pragma unroll
     for (int i = 1; i < R; ++i) s.add(s_m[i], s_l[i], s_o[i][c]);
-    const int64_t nh = n * a.H + b.first + q;
     store4((typename Tile::Out *)a.out + nh * D + 4 * c, divided(s.o, s.l));
     if (c == 0) a.lse[nh] = s.lse();
 }
 
 // ------------------------------------------------------------------- host
 
-// Longest rows that the direct way takes, in bytes of keys and values.
-constexpr int64_t kDirectBytes = 384 << 10;
-
-bool is_direct(int64_t longest, const sa_paged_cache &c) {
-    const int64_t es = c.dtype == SA_FP32 ? 4 : c.dtype == SA_BF16 ? 2 : 1;
-    return longest * 2 * c.D * es <= kDirectBytes;
-}
-
 int64_t longest_row(const sa_graph_s *g) {
     int64_t n = g->kind == 0 ? (int64_t)g->W + g->n_off
                              : (int64_t)g->W + g->max_resid;
     return n < g->T ? n : g->T;
+}
+
+// Rows that the direct way takes, by the bytes of keys and values of the longest.
+// Below kDirectBytes it is the faster one whatever the batch (8 rows of 128 KB:
+// 8.3 us against 12.5, of 512 KB: 14.4 and 14.5; 2,048 rows of 128 KB: 61 and 71,
+// of 384 KB: 158 and 156).  Rows that nearly all have the window's length and
+// fill the SMs in one go are better left whole up to kDirectUniform (128 rows of
+// 1 MB: 27 against 35 us, of 2 MB: 46 against 55; 160 rows of 512 KB: 27
+// against 25, for they take two goes).
+constexpr int64_t kDirectBytes = 384 << 10, kDirectUniform = 2 << 20;
+
+int64_t longest_bytes(const sa_graph_s *g, const sa_paged_cache &c) {
+    return longest_row(g) * 2 * c.D * (c.dtype == SA_FP32 ? 4 : c.dtype == SA_BF16 ? 2 : 1);
+}
+
+bool is_direct(const sa_graph_s *g, const sa_paged_cache &c, int64_t rows, int sms) {
+    const int64_t bytes = longest_bytes(g, c);
+    if (bytes <= kDirectBytes) return true;
+    const bool uniform = g->kind == 0 && g->W <= g->T / 4;
+    return bytes <= kDirectUniform && uniform && rows <= sms && 4 * rows >= 3 * sms;
 }
 
 // f(a Tile type) for this cache and group size.
@@ -1113,18 +1113,18 @@ Plan split_plan(int sms) {
 }
 
 template <typename Tile>
-sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, bool direct,
-                        void *workspace,
-                        cudaStream_t s) {
+sa_status launch_decode(DecodeArgs &a, const sa_graph_s *graph, const sa_paged_cache &cache,
+                        void *workspace, cudaStream_t s) {
     using M = Layout<Tile>;
     a.QB = (a.G + Tile::NQ - 1) / Tile::NQ;
-    if (direct) {
-        const int64_t blocks = a.N * a.Hkv * a.QB;
+    const GraphView g = make_view(graph);
+    const int64_t blocks = a.N * a.Hkv * a.QB, longest = longest_row(graph);
+    int sms = 0;
+    SA_CUDA_TRY(sa_sm_count(&sms));
+    if (is_direct(graph, cache, blocks, sms)) {
         if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
         // a warp for each tile, but no more warps than the GPU holds: with many
         // rows, several CTAs of few warps overlap one's start with another's work
-        int sms = 0;
-        SA_CUDA_TRY(sa_sm_count(&sms));
         const int64_t held = (int64_t)Tile::kWarps * Tile::kOcc * sms;
         int64_t nw = (longest + Tile::KT - 1) / Tile::KT;
         if (nw > (held + blocks - 1) / blocks) nw = (held + blocks - 1) / blocks;
@@ -1137,8 +1137,6 @@ sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, bool
         SA_CUDA_TRY(cudaGetLastError());
         return SA_OK;
     }
-    int sms = 0;
-    SA_CUDA_TRY(sa_sm_count(&sms));
     const Plan p = split_plan<Tile>(sms);
     a.warp_part = (float *)workspace;
     a.cta_part = a.warp_part + p.ctas * p.warps * p.part_floats;
@@ -1168,7 +1166,7 @@ sa_status launch_decode(DecodeArgs &a, const GraphView &g, int64_t longest, bool
 size_t sa_paged_decode_workspace(const sa_tensor *q, const sa_paged_cache &c,
                                  const sa_graph_s *g) {
     int sms = 0;
-    if (is_direct(longest_row(g), c) || sa_sm_count(&sms) != cudaSuccess) return 0;
+    if (longest_bytes(g, c) <= kDirectBytes || sa_sm_count(&sms) != cudaSuccess) return 0;
     return with_tile(c, q->H / c.Hkv, [&](auto *t) {
         return split_plan<std::remove_pointer_t<decltype(t)>>(sms);
     }).bytes();
@@ -1200,13 +1198,11 @@ sa_status sa_paged_decode(const sa_tensor *q, const sa_paged_cache &c, const int
     a.lse = lse;
     a.err = sa_device_error_word();
     if (!a.err) return SA_ERR_CUDA;
-    const GraphView gv = make_view(g);
-    const int64_t longest = longest_row(g);
     struct Result {
         sa_status st = SA_ERR_UNSUPPORTED;
     };
     return with_tile(c, a.G, [&](auto *t) {
         return Result{launch_decode<std::remove_pointer_t<decltype(t)>>(
-            a, gv, longest, is_direct(longest, c), workspace, s)};
+            a, g, c, workspace, s)};
     }).st;
 }
