@@ -37,8 +37,8 @@
 //           warps take equal runs and merge in shared memory.
 //   split   the tiles of all rows, end to end, are cut into equal runs for all
 //           warps of the GPU, wherever rows begin or end.  Whole rows are
-//           finished by their warp; rows that are cut leave (m, l, acc), merged
-//           first by the CTA and then, across CTAs, by a second small kernel.
+//           finished by their warp; rows that are cut leave (m, l, acc), which
+//           a second small kernel joins.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -153,6 +153,23 @@ __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 
 
 // --------------------------------------------------------------- arguments
 
+// A row that a warp starts and others go on with: its first query head, the warp
+// (of nw in a CTA), and its parts: `head` of them by warps of that CTA, then one
+// from each of `mid` CTAs that have nothing else, then `tail` by the first warps
+// of the next (head = 0: there is no such row).
+struct __align__(16) Cut {
+    int64_t nh;
+    int32_t warp, head, mid, tail;
+    int16_t gq, nw;
+    __device__ __forceinline__ int count() const { return head + mid + tail; }
+    // slot of part i
+    __device__ __forceinline__ int64_t slot(int i) const {
+        if (i < head) return 2 * ((int64_t)warp + i) + (i == 0 ? 1 : 0);
+        const int cta = warp / nw + 1 + min(i - head, mid);
+        return 2 * ((int64_t)cta * nw + max(i - head - mid, 0));
+    }
+};
+
 struct DecodeArgs {
     const void *q, *k, *v;
     const float *k_scale, *v_scale;
@@ -164,8 +181,8 @@ struct DecodeArgs {
     float scale2;           // scale * log2(e)
     void *out;
     float *lse;
-    float *warp_part, *cta_part;  // partial rows: slots [warp], [CTA][2]
-    int4 *cut;  // per CTA: first query head, last CTA and queries of the row that goes on
+    float *part;  // partial rows [warp][2]: of the row it goes on with, of the one it starts
+    Cut *cut;     // [warp]
     int *err;
 };
 
@@ -778,26 +795,23 @@ __device__ __forceinline__ void write_part(Tile &tile, float *slot) {
     });
 }
 
-// Merge of `count` parts of a row by `threads` threads, into another part or
-// (to == nullptr) the output.  Parts are entry `first` of the list, then every
-// second one from the next even.  (Not inlined: code that runs once costs its
-// fetch.)
+// A row's output, or (with `to`) one part, from `count` parts by `threads`
+// threads.  (Not inlined: code that runs once costs its fetch.)
 template <typename Out, int NQ, int D>
-__device__ __noinline__ void merge_parts(int tid, int threads, const float *const *list, int first,
-                                         int count, int gq, float *to, Out *out, float *lse) {
+__device__ __noinline__ void merge_parts(int tid, int threads, const float *const *part, int count,
+                                         int gq, float *to, Out *out, float *lse) {
     constexpr int C = D / 4;
-    auto part = [&](int k) { return list[k ? (first & ~1) + 2 * k : first]; };
 #pragma unroll 1
     for (int x = tid; x < gq * C; x += threads) {
         const int q = x / C, c = x % C;
         float m = -INFINITY, l = 0.f;
 #pragma unroll 4
-        for (int k = 0; k < count; ++k) m = fmaxf(m, part(k)[q]);
+        for (int k = 0; k < count; ++k) m = fmaxf(m, part[k][q]);
         const float base = finite_base(m);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
         for (int k = 0; k < count; ++k) {
-            const float *p = part(k);
+            const float *p = part[k];
             const float w = ex2(p[q] - base);
             const float4 y = *reinterpret_cast<const float4 *>(p + Part<NQ, D>::place(q, c));
             l = fmaf(w, p[NQ + q], l);
@@ -807,10 +821,10 @@ __device__ __noinline__ void merge_parts(int tid, int threads, const float *cons
         if (to) {
             *reinterpret_cast<float4 *>(to + Part<NQ, D>::place(q, c)) = o;
             if (c == 0) to[q] = m, to[NQ + q] = l;
-        } else {
-            store4(out + q * D + 4 * c, divided(o, l));
-            if (c == 0) lse[q] = l == 0.f ? -INFINITY : (base + lg2(l)) * kLn2;
+            continue;
         }
+        store4(out + q * D + 4 * c, divided(o, l));
+        if (c == 0) lse[q] = l == 0.f ? -INFINITY : (base + lg2(l)) * kLn2;
     }
 }
 
@@ -820,7 +834,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     paged_decode_direct(DecodeArgs a, GraphView g) {
     using M = Layout<Tile>;
     extern __shared__ __align__(128) uint8_t mem[];
-    __shared__ const float *s_part[2 * Tile::kWarps];
+    __shared__ const float *s_part[Tile::kWarps];
     const int U = a.Hkv * a.QB, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int64_t n = blockIdx.x / U;
     const Block b = block_of<Tile::NQ>(a, blockIdx.x % U);
@@ -833,11 +847,11 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     Tile tile;
     run_edges(tile, a, g, t, n, b, x0, x1, own);
     write_part(tile, (float *)own);
-    if ((threadIdx.x & 31) == 0) s_part[2 * warp] = (float *)own;
+    if ((threadIdx.x & 31) == 0) s_part[warp] = (float *)own;
     __syncthreads();
     const int64_t nh = n * a.H + b.first;
     merge_parts<typename Tile::Out, Tile::NQ, Tile::D>(
-        threadIdx.x, blockDim.x, s_part, 0, nw, b.gq, nullptr,
+        threadIdx.x, blockDim.x, s_part, nw, b.gq, nullptr,
         (typename Tile::Out *)a.out + nh * Tile::D, a.lse + nh);
 }
 
@@ -855,14 +869,6 @@ struct Shares {
 // What the start of a row costs a warp (positions, pages and the first copies
 // one after the other, then the merge), in tiles.  The shares count it.
 constexpr int kRowStart = 3;
-// A cut row's parts in a CTA: the row's first query head, entry of the first part
-// and number of parts, queries, the row's last CTA, whether it starts and ends here.
-struct Cut {
-    int64_t nh;
-    int first, count, gq, last;
-    bool starts, ends;
-};
-
 // Fewest tiles worth a warp: below, a share is mostly its own start and merge.
 constexpr int kLeastTiles = 4;
 
@@ -876,11 +882,8 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     extern __shared__ __align__(128) uint8_t mem[];
     __shared__ int64_t s_start[NT + 1];  // row tiles before each thread's rows
     __shared__ int64_t s_sum[NW];
-    // parts of cut rows: of the row that each warp goes on with and of the one that it
-    // starts; then each warp's ring
-    __shared__ const float *s_part[4 * NW];
-    // cut rows with parts in this CTA: the one it goes on with, those its warps start
-    __shared__ Cut s_cut[1 + NW];
+    __shared__ const float *s_part[NW];  // each warp's ring
+    __shared__ int s_inside;             // queries of the row that has the whole CTA, or 0
     asm volatile("griddepcontrol.launch_dependents;");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t U = (int64_t)a.Hkv * a.QB;
@@ -900,11 +903,10 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
             if (lane >= o) x += y;
         }
         if (lane == 31) s_sum[warp] = x;
-        if (tid <= NW) s_cut[tid].count = 0;
         __syncthreads();
         for (int w = 0; w < warp; ++w) x += s_sum[w];
         s_start[tid + 1] = x;
-        if (tid == 0) s_start[0] = 0;
+        if (tid == 0) s_start[0] = 0, s_inside = 0;
         __syncthreads();
     }
     const int64_t total = s_start[NT] * U;
@@ -915,6 +917,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     int64_t x = warp < nw ? shares.begin(W) : 0;
     const int64_t x_end = warp < nw ? shares.begin(W + 1) : 0;
     uint8_t *own = mem + warp * M::kBytes;
+    if (lane == 0) a.cut[blockIdx.x * NW + warp].head = 0;
     if (x < x_end) {
         // the row of tile x
         const int64_t y = quotient(x, U);
@@ -958,31 +961,44 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
                 const Block b = block_of<Tile::NQ>(a, u);
                 run_edges(tile, a, g, t, n, b, tile0 * KT, min(t.deg, tile1 * KT), own);
                 const bool goes_on = tile0 > 0, ends = tile1 == tiles;
-                // (the ring is free, but not for long if more rows follow)
-                const bool whole = !goes_on && ends, stays = x + (to - from) >= x_end;
-                float *part = whole || stays ? (float *)own : a.warp_part + W * PF;
-                write_part(tile, part);
-                if (whole) {
-                    const int64_t nh = n * a.H + b.first;
-                    if (lane == 0) s_part[2 * (NW + warp)] = part;
-                    __syncwarp();
-                    merge_parts<Out, Tile::NQ, D>(lane, 32, s_part, 2 * (NW + warp), 1, b.gq, nullptr,
+                write_part(tile, (float *)own);
+                __syncwarp();
+                const int64_t nh = n * a.H + b.first;
+                // the row's first tile and its end, in the shares' coordinate
+                const int64_t row0 = x - from + kRowStart, row1 = row0 + tiles;
+                const bool inside = nw == NW && row0 < shares.begin(W - warp) &&
+                                    row1 >= shares.begin(W - warp + nw);
+                if (lane == 0) {
+                    s_part[warp] = (const float *)own;
+                    if (inside) s_inside = b.gq;
+                }
+                __syncwarp();
+                if (!goes_on && ends) {
+                    merge_parts<Out, Tile::NQ, D>(lane, 32, s_part + warp, 1, b.gq, nullptr,
                                                   (Out *)a.out + nh * D, a.lse + nh);
-                    __syncwarp();
-                } else {
-                    const int entry = 2 * warp + (goes_on ? 0 : 1);
-                    if (lane == 0) {
-                        s_part[entry] = part;
-                        if (!goes_on || warp == 0) {
-                            // the CTA's first part: it knows how far the row reaches
-                            const int64_t end = shares.of(x - from + tiles + kRowStart - 1);
-                            const int64_t here = min(end, W - warp + nw - 1);
-                            s_cut[goes_on ? 0 : 1 + warp] =
-                                Cut{n * a.H + b.first, entry, (int)(here - W) + 1, b.gq,
-                                    (int)quotient(end, nw), !goes_on, here == end};
-                        }
+                } else if (!inside) {
+                    float4 *part =
+                        reinterpret_cast<float4 *>(a.part + (W * 2 + (goes_on ? 0 : 1)) * PF);
+                    for (int i = lane; i < (2 * Tile::NQ + b.gq * D) / 4; i += 32)
+                        part[i] = reinterpret_cast<const float4 *>(own)[i];
+                    if (!goes_on) {
+                        const int64_t last = shares.of(row1 - 1), cta = quotient(last, nw);
+                        // (CTAs of fewer warps merge nothing)
+                        const int64_t next = nw < NW ? last + 1 : W - warp + nw;
+                        Cut cut;
+                        cut.nh = nh;
+                        cut.warp = (int32_t)W;
+                        cut.head = (int32_t)(min(last + 1, next) - W);
+                        cut.mid = last < next ? 0 : (int32_t)cta - (int32_t)blockIdx.x - 1;
+                        cut.tail = last < next ? 0 : (int32_t)(last + 1 - cta * nw);
+                        if (cut.tail == NW && row1 == shares.begin(last + 1))
+                            cut.tail = 0, ++cut.mid;  // nothing else in that CTA
+                        cut.gq = (int16_t)b.gq;
+                        cut.nw = (int16_t)nw;
+                        if (lane == 0) a.cut[blockIdx.x * NW + warp] = cut;
                     }
                 }
+                __syncwarp();
             }
             x += to - from;
             if (x >= x_end) break;
@@ -994,54 +1010,63 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
             }
         }
     }
+    // a long row's parts in this CTA become one
     __syncthreads();
-
-    // each row's parts in this CTA become one, or the output
-    int4 cut = make_int4(-1, -1, 0, 0);
-#pragma unroll 1
-    for (int i = 0; i <= NW; ++i) {
-        const Cut c = s_cut[i];
-        if (c.count == 0) continue;
-        float *to = c.starts && c.ends
-                        ? nullptr
-                        : a.cta_part + ((int64_t)blockIdx.x * 2 + (c.starts ? 1 : 0)) * PF;
-        merge_parts<Out, Tile::NQ, D>(tid, NT, s_part, c.first, c.count, c.gq, to,
-                                      (Out *)a.out + c.nh * D, a.lse + c.nh);
-        if (c.starts && !c.ends)
-            cut = make_int4((int)c.nh, (int)(c.nh >> 32), c.last, c.gq);
-    }
-    if (tid == 0) a.cut[blockIdx.x] = cut;
+    if (s_inside)
+        merge_parts<Out, Tile::NQ, D>(tid, NT, s_part, NW, s_inside,
+                                      a.part + (int64_t)blockIdx.x * NW * 2 * PF, (Out *)nullptr,
+                                      nullptr);
 }
 
-// The rows cut between CTAs: block (c, q) joins query q of the row that starts
-// in CTA c and goes on.
-constexpr int kJoinThreads = 256;
+// The cut rows: block (c, q) joins query q of those that CTA c's warps start.
+// The block's lane groups, a row of D columns each, are shared among them.
+constexpr int kJoinThreads = 512;
 
 template <typename Tile>
 __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) {
-    constexpr int NQ = Tile::NQ, D = Tile::D, C = D / 4, R = kJoinThreads / C;
-    constexpr int PF = Part<NQ, D>::kFloats;
+    constexpr int NQ = Tile::NQ, D = Tile::D, C = D / 4, R = kJoinThreads / C, NW = Tile::kWarps;
+    using P = Part<NQ, D>;
+    static_assert(NW <= R && NW <= 32, "a group for each row");
+    __shared__ Cut s_cut[NW];
+    __shared__ int s_count;
     __shared__ float s_m[R], s_l[R];
     __shared__ float4 s_o[R][C];
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int4 cut = __ldcg(a.cut + blockIdx.x);
-    const int q = blockIdx.y, c = threadIdx.x % C, r = threadIdx.x / C;
-    if (q >= cut.w) return;
-    const int64_t nh = ((int64_t)(uint32_t)cut.x | ((int64_t)cut.y << 32)) + q;
-    const int count = cut.z - (int)blockIdx.x + 1;
+    if (threadIdx.x < 32) {
+        const int lane = threadIdx.x;
+        Cut cut = {};
+        if (lane < NW) {
+            const int4 *p = reinterpret_cast<const int4 *>(a.cut + blockIdx.x * NW + lane);
+            int4 *to = reinterpret_cast<int4 *>(&cut);
+            to[0] = __ldcg(p), to[1] = __ldcg(p + 1);
+        }
+        const unsigned there = __ballot_sync(kFull, cut.head > 0);
+        if (cut.head > 0) s_cut[__popc(there & ((1u << lane) - 1))] = cut;
+        if (lane == 0) s_count = __popc(there);
+    }
+    __syncthreads();
+    if (s_count == 0) return;
+    int each = R;  // groups of a row: a power of two
+    while (each * s_count > R) each >>= 1;
+    const int q = blockIdx.y, c = threadIdx.x % C, g = threadIdx.x / C;
+    const int which = g / each, r = g % each;
+    Cut cut = {};
+    if (which < s_count) cut = s_cut[which];
+    const int count = q < cut.gq ? cut.count() : 0;
     State s;
 #pragma unroll 4
-    for (int i = r; i < count; i += R) {
-        const float *p = a.cta_part + (((int64_t)blockIdx.x + i) * 2 + (i == 0 ? 1 : 0)) * PF;
+    for (int i = r; i < count; i += each) {
+        const float *p = a.part + cut.slot(i) * P::kFloats;
         s.add(__ldcg(p + q), __ldcg(p + NQ + q),
-              __ldcg(reinterpret_cast<const float4 *>(p + Part<NQ, D>::place(q, c))));
+              __ldcg(reinterpret_cast<const float4 *>(p + P::place(q, c))));
     }
-    if (c == 0) s_m[r] = s.m, s_l[r] = s.l;
-    s_o[r][c] = s.o;
+    if (c == 0) s_m[g] = s.m, s_l[g] = s.l;
+    s_o[g][c] = s.o;
     __syncthreads();
-    if (r != 0) return;
-#pragma unroll
-    for (int i = 1; i < R; ++i) s.add(s_m[i], s_l[i], s_o[i][c]);
+    if (r != 0 || count == 0) return;
+#pragma unroll 4
+    for (int i = g + 1; i < g + each; ++i) s.add(s_m[i], s_l[i], s_o[i][c]);
+    const int64_t nh = cut.nh + q;
     store4((typename Tile::Out *)a.out + nh * D + 4 * c, divided(s.o, s.l));
     if (c == 0) a.lse[nh] = s.lse();
 }
@@ -1099,7 +1124,7 @@ auto with_tile(const sa_paged_cache &c, int64_t G, F f)
 struct Plan {
     int64_t ctas = 0, part_floats = 0, warps = 0;
     size_t bytes() const {
-        return ctas ? (size_t)(ctas * (warps + 2) * part_floats * 4 + ctas * 16) : 0;
+        return ctas ? (size_t)(ctas * warps) * (2 * part_floats * 4 + sizeof(Cut)) : 0;
     }
 };
 
@@ -1138,9 +1163,8 @@ sa_status launch_decode(DecodeArgs &a, const sa_graph_s *graph, const sa_paged_c
         return SA_OK;
     }
     const Plan p = split_plan<Tile>(sms);
-    a.warp_part = (float *)workspace;
-    a.cta_part = a.warp_part + p.ctas * p.warps * p.part_floats;
-    a.cut = (int4 *)(a.cta_part + p.ctas * 2 * p.part_floats);
+    a.part = (float *)workspace;
+    a.cut = (Cut *)(a.part + p.ctas * p.warps * 2 * p.part_floats);
     SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_split<Tile>, Tile::kWarps * M::kBytes));
     SA_LAUNCH("paged_decode", s,
               paged_decode_split<Tile>
