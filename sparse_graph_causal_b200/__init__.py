@@ -429,7 +429,7 @@ def sparse_attn_paged_plan(length, n_new, block_table, free_pages, free_count, p
     len_p = _array(length, "length", i64, (B,), dev)
     count_p = _array(free_count, "free_count", i64, (1,), dev)
     d = SaPagedStep(
-        B, M, page_size, batch._shape[1], n_stack, len_p, _array(n_new, "n_new", i32, (B,), dev),
+        B, M, int(page_size), batch._shape[1], n_stack, len_p, _array(n_new, "n_new", i32, (B,), dev),
         _array(block_table, "block_table", i32, shape, dev),
         _array(free_pages, "free_pages", i32, (n_stack,), dev), count_p,
         len_p if length_out is None else _array(length_out, "length_out", i64, (B,), dev),

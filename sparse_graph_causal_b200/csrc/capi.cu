@@ -640,6 +640,7 @@ sa_status sparse_attn_paged_decode(const sa_tensor *q, const sa_paged_cache *cac
     if ((st = check_paged_rows(q, cache)) != SA_OK || (st = check_tensor(out, q)) != SA_OK)
         return st;
     if (q->H % cache->Hkv != 0 || rows < 1 || max_pages < 1) return SA_ERR_INVALID_ARG;
+    if (q->H > 1 << 24) return SA_ERR_UNSUPPORTED;
     if (!array_ok(block_table, 4) || !array_ok(pos, 8) || !aligned(row, 4) ||
         !array_ok(lse, 16) || !std::isfinite(scale))
         return SA_ERR_INVALID_ARG;

@@ -407,6 +407,43 @@ def test_decode_full_causal(sa, pos, H, Hkv, D, T, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("H, Hkv, D, pos", [
+    (8, 2, 128, [60000, 12, 45001, 59999]), (32, 2, 64, [52345, -1, 60000]),
+    (12, 1, 32, [60000, 59000, 0, 33333, 60000, 45000]), (4, 4, 64, [59999, 3, 40000]),
+])
+def test_decode_rows_over_many_ctas(sa, H, Hkv, D, pos, dtype):
+    c = Case(pos, H, Hkv, D, 64, dtype, 60001, 60001)
+    c.check(*c.run(sa))
+    sa.sparse_attn_check_device()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("seed", range(8))
+def test_decode_batches_of_any_shape(sa, seed, dtype):
+    """Rows of all lengths in one batch, windows that cut some of them, heads of all groups: the
+    shares' borders fall anywhere."""
+    rng = np.random.default_rng(100 + seed)
+    N = int(np.exp(rng.uniform(0, np.log(60))))
+    T = int(rng.integers(3000, 30000))
+    pos = np.exp(rng.uniform(0, np.log(T), N)).astype(np.int64) - 1
+    pos[rng.integers(N)] = T - 1
+    D, Hkv = int(rng.choice([32, 64, 128])), int(rng.choice([1, 2, 3]))
+    G, page = int(rng.choice([1, 2, 5, 8, 12, 20])), int(rng.integers(5, 80))
+    W = T if seed % 2 else int(rng.integers(2000, T))
+    c = Case(pos, Hkv * G, Hkv, D, page, dtype, T, W, range(15), seed=seed)
+    c.check(*c.run(sa))
+    sa.sparse_attn_check_device()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_decode_window_rows_fill_the_gpu(sa, dtype):
+    """120 windows of equal length: one row for each SM."""
+    rng = np.random.default_rng(9)
+    c = Case(rng.integers(2500, 9000, 60), 4, 2, 64, 16, dtype, 9000, 2100)
+    c.check(*c.run(sa), skip=set(range(60)) - set(range(0, 60, 7)))
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 def test_decode_many_tokens(sa, dtype):
     rng = np.random.default_rng(2)
     pos = rng.integers(-1, 600, 700)
@@ -659,6 +696,104 @@ def test_captured_step_advances(sa, W, dtype):
     assert torch.equal(a["length"], b["length"]) and int(a["length"][0]) == len(steps)
     assert torch.equal(a["table"], b["table"]) and torch.equal(a["count"], b["count"])
     sa.sparse_attn_check_device()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_captured_decode_of_long_rows(sa, dtype):
+    """Rows cut over the GPU in a captured graph: replays follow the positions in place."""
+    c = Case([20000, 15000, 77], 8, 2, 64, 16, dtype, 20001, 20001)
+    g, cache, table = c.graph(sa), c.cache(sa), _gpu(c.table, torch.int32)
+    need = sa.sparse_attn_paged_decode_workspace_size(c.q, cache, g)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    pos = _gpu(c.pos, torch.int64)
+    out, lse = torch.zeros_like(c.q), torch.zeros(c.q.shape[:2], device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        sa.sparse_attn_paged_decode(c.q, cache, table, pos, g, c.scale, out=out, lse=lse,
+                                    workspace=ws)
+    for p in ([20000, 15000, 77], [5, 15000, -1], [19999, 0, 76]):
+        pos.copy_(torch.tensor(p))
+        graph.replay()
+        o, l = sa.sparse_attn_paged_decode(c.q, cache, table, pos, g, c.scale)
+        assert torch.equal(out, o) and torch.equal(lse, l)
+    c.pos = np.array(p)
+    c.keys = [_keys(x, 20001, 20001, (), None) for x in p]
+    c.check(out, lse)
+    sa.sparse_attn_check_device()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+def test_cache_of_more_than_32_bits(sa, dtype):
+    """Rows whose offsets, in elements, are above 2^32: written by append, read by decode."""
+    Hkv, page, D = 8, 64, 128
+    n_pages = (1 << 32) // (Hkv * page * D) + 70
+    if torch.cuda.mem_get_info()[0] < 3 * n_pages * Hkv * page * D * (4 if dtype == "fp32" else 2):
+        pytest.skip("not enough device memory")
+    kv = [torch.empty((n_pages, Hkv, page, D), device="cuda", dtype=TYPES[dtype])
+          for _ in range(2)]
+    scales = [torch.empty((n_pages, Hkv, page), device="cuda") if dtype == "e4m3" else None
+              for _ in range(2)]
+    cache = sa.PagedCache(*kv, *scales)
+    T, qt = 4000, torch.float32 if dtype == "fp32" else torch.bfloat16
+    M = -(-T // page)
+    table = torch.arange(n_pages - M, n_pages, dtype=torch.int32, device="cuda").flip(0)[None]
+    table = table.contiguous()
+    gen = torch.Generator("cuda")
+    gen.manual_seed(6)
+    k, v = (torch.empty((T, Hkv, D), device="cuda").normal_(generator=gen).to(qt)
+            for _ in range(2))
+    at = torch.arange(T, device="cuda")
+    slot = table[0].long()[at // page] * page + at % page
+    assert int(slot.min()) * D * Hkv > 1 << 32
+    sa.sparse_attn_paged_append(k, v, cache, slot)
+    q = torch.empty((1, 8, 1, D), device="cuda").normal_(generator=gen).to(qt)
+    pos = torch.tensor([T - 1], device="cuda")
+    for W in (200, T):
+        g = sa.sparse_attn_graph_build_structured(T, W, [])
+        out, lse = sa.sparse_attn_paged_decode(q, cache, table, pos, g, 0.125)
+        sa.sparse_attn_check_device()
+        for h in range(Hkv):
+            rows = []
+            for x in (k, v):
+                x = x[T - W:, h].double().cpu().numpy()
+                if dtype == "e4m3":
+                    y, unit = paged_ref.quantise(x)
+                    x = y * unit.astype(np.float64)[..., None]
+                rows.append(x)
+            qd = q[0, h:h + 1, 0].double().cpu().numpy()
+            o, l, size, vmax = paged_ref.attend(qd, *rows, 0.125)
+            t_lse, t_out, rel = paged_ref.tolerances(W, D, size, vmax, qt)
+            assert (np.abs(out[0, h].double().cpu().numpy() - o) <= t_out + rel * np.abs(o)).all()
+            assert abs(float(lse[0, h]) - l[0]) <= t_lse + 2.0 ** -24 * abs(l[0])
+
+
+@pytest.mark.parametrize("W", [32, 3000])
+def test_decode_scales_of_all_sizes(sa, W):
+    """Value scales from 2^-40 to 2^40 in one row: the weights keep their own range."""
+    c = Case([2999, 1111], 8, 2, 64, 16, "e4m3", 3000, W, range(12))
+    gen = torch.Generator("cuda")
+    gen.manual_seed(2)
+    codes, s = c.pool[1]
+    size = torch.randint(-40, 41, s.shape, device="cuda", generator=gen)
+    for lo, hi in ((-40, 41), (-40, -30), (30, 41)):
+        c.pool[1] = (codes, s * torch.exp2(size.clamp(lo, hi).float()))
+        c.check(*c.run(sa))
+    # rows of zeros have scale 0; a row of NaN scale reaches the tokens that see it
+    c.pool[1] = (codes, torch.where(s.isnan(), s, 0.0))
+    out, lse = c.run(sa)
+    assert not out.any() and torch.isfinite(lse).all()
+
+
+def test_decode_flags_positions_past_the_table(sa):
+    c = Case([400, 99], 2, 1, 64, 16, "bf16", 1000, 32)
+    table = _gpu(c.table[:, :25], torch.int32)          # 25 pages: positions below 400
+    out, lse = sa.sparse_attn_paged_decode(c.q, c.cache(sa), table, _gpu(c.pos, torch.int64),
+                                           c.graph(sa), c.scale)
+    with pytest.raises(sa.SparseAttentionError):
+        sa.sparse_attn_check_device()
+    assert not out[0].any() and torch.isneginf(lse[0]).all()
+    c.check(out, lse, skip=(0,))
 
 
 def test_decode_on_two_streams_at_once(sa):
