@@ -113,6 +113,22 @@ class _LazyLib:
 _lib = _LazyLib()
 
 
+class _LazyPaged:
+    """The module that marshals the paged cache's calls, loaded on first use
+    (its import then takes this name)."""
+
+    def __getattr__(self, name):
+        import importlib
+        try:
+            return getattr(importlib.import_module(__name__ + "._paged"), name)
+        except ModuleNotFoundError as e:
+            raise ImportError("the _paged module is not built: run "
+                              "`python -m sparse_graph_causal_b200.build`") from e
+
+
+_paged = _LazyPaged()
+
+
 class SparseAttentionError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -342,19 +358,6 @@ def _array(t, name: str, dtype, shape, index: int) -> int:
     return t.data_ptr()
 
 
-def _call_on(index: int, stream, where: str, fn, *args):
-    """fn(*args, stream) with the tensors' device current (the library launches
-    on the current one), on its current stream unless one is given."""
-    if index == torch._C._cuda_getDevice():
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(index) if stream is None
-                    else _stream(stream))
-    else:
-        with torch.cuda.device(index):
-            status = fn(*args, _stream(stream))
-    if status != SA_OK:
-        _check(status, where)
-
-
 class PagedCache:
     """Key and value pages [n_pages, Hkv, page_size, D] (bf16, fp32, or
     float8_e4m3fn with fp32 scales [n_pages, Hkv, page_size]) of one layer."""
@@ -377,6 +380,7 @@ class PagedCache:
         self._desc = SaPagedCache(kp, vp, ks, vs, _PAGED_DTYPES[k.dtype], n, self._heads,
                                   self._page, self._dim)
         self._index, self._ref = index, ctypes.byref(self._desc)
+        self._address = ctypes.addressof(self._desc)
 
     k = property(lambda self: self._tensors[0])
     v = property(lambda self: self._tensors[1])
@@ -399,8 +403,10 @@ class PagedBatch:
                          new(B, torch.int32))
         if not self._tensors[0].is_cuda:
             raise ValueError("a PagedBatch lies on a CUDA device")
-        self._shape = B, capacity, self._tensors[0].get_device()
-        self._addresses = tuple(t.data_ptr() for t in self._tensors)
+        cu_new, slot, pos, row, status = (t.data_ptr() for t in self._tensors)
+        self._desc = SaPagedStep(B=B, capacity=capacity, cu_new=cu_new, slot=slot, pos=pos, row=row,
+                                 status=status)
+        self._index, self._address = self._tensors[0].get_device(), ctypes.addressof(self._desc)
 
     cu_new = property(lambda self: self._tensors[0])
     slot = property(lambda self: self._tensors[1])
@@ -418,43 +424,14 @@ def sparse_attn_paged_plan(length, n_new, block_table, free_pages, free_count, p
     free_count (int64 [1]) pages.  block_table and free_pages are updated in
     place, and so are length and free_count unless length_out and
     free_count_out are given.  Returns batch."""
-    if not isinstance(block_table, torch.Tensor) or not block_table.is_cuda \
-            or block_table.dim() != 2:
-        raise ValueError("block_table must be a CUDA int32 [B, max_pages] tensor")
-    B, M = shape = block_table.shape
-    dev, i64, i32 = block_table.get_device(), torch.int64, torch.int32
-    if batch._shape[0] != B or batch._shape[2] != dev:
-        raise ValueError(f"batch must be made for {B} requests on cuda:{dev}")
-    n_stack = free_pages.numel() if isinstance(free_pages, torch.Tensor) else 0
-    len_p = _array(length, "length", i64, (B,), dev)
-    count_p = _array(free_count, "free_count", i64, (1,), dev)
-    d = SaPagedStep(
-        B, M, int(page_size), batch._shape[1], n_stack, len_p, _array(n_new, "n_new", i32, (B,), dev),
-        _array(block_table, "block_table", i32, shape, dev),
-        _array(free_pages, "free_pages", i32, (n_stack,), dev), count_p,
-        len_p if length_out is None else _array(length_out, "length_out", i64, (B,), dev),
-        count_p if free_count_out is None else
-        _array(free_count_out, "free_count_out", i64, (1,), dev), *batch._addresses)
-    _call_on(dev, stream, "sparse_attn_paged_plan", _lib.sparse_attn_paged_plan, ctypes.byref(d))
+    if not isinstance(batch, PagedBatch):
+        raise ValueError("batch must be a PagedBatch")
+    status = _paged.plan(length, n_new, block_table, free_pages, free_count, page_size,
+                         batch._address, batch._index, length_out, free_count_out,
+                         None if stream is None else _stream(stream))
+    if status != SA_OK:
+        _check(status, "sparse_attn_paged_plan")
     return batch
-
-
-def _token_rows(t, name: str, cache: PagedCache):
-    """New rows [N, Hkv, D] or [N, Hkv, 1, D] with any stride between tokens:
-    the descriptor and that stride."""
-    H, D = cache._heads, cache._dim
-    if not isinstance(t, torch.Tensor) or t.get_device() != cache._index:
-        raise ValueError(f"{name} must be a tensor on {cache.device}")
-    if t.dim() == 4 and t.shape[2] == 1:
-        t = t[:, :, 0]
-    shape, stride = t.shape, t.stride()
-    if len(shape) != 3 or shape[1] != H or shape[2] != D or stride[2] != 1 \
-            or (H > 1 and stride[1] != D):
-        raise ValueError(f"{name} must be [N, {H}, {D}] with contiguous heads")
-    dt = _PAGED_DTYPES.get(t.dtype, -1)
-    if dt == SA_E4M3:
-        raise ValueError(f"{name}: new rows are bf16 or fp32")
-    return SaTensor(t.data_ptr(), dt, shape[0], H, 1, D), stride[0] if shape[0] > 1 else H * D
 
 
 def sparse_attn_paged_append(k_new, v_new, cache: PagedCache, slot, stream=None):
@@ -462,16 +439,20 @@ def sparse_attn_paged_append(k_new, v_new, cache: PagedCache, slot, stream=None)
     between tokens is free) to the cache rows slot int64 [N]; negative slots
     are skipped.  bf16 rows are rounded to 8 bits, one scale per row, for a
     float8_e4m3fn cache."""
-    (tk, sk), (tv, sv) = _token_rows(k_new, "k_new", cache), _token_rows(v_new, "v_new", cache)
-    ps = _array(slot, "slot", torch.int64, (tk.B,), cache._index)
-    if tk.B == 0 and tv.B == 0:
-        return
-    _call_on(cache._index, stream, "sparse_attn_paged_append", _lib.sparse_attn_paged_append,
-             ctypes.byref(tk), sk, ctypes.byref(tv), sv, ps, cache._ref)
+    status = _paged.append(k_new, v_new, cache._address, cache._index, slot,
+                           None if stream is None else _stream(stream))
+    if status != SA_OK:
+        _check(status, "sparse_attn_paged_append")
+
+
+def _paged_queries(q, cache: PagedCache):
+    if not isinstance(q, torch.Tensor) or q.get_device() != cache._index or q.dim() != 4:
+        raise ValueError(f"q must be an [N, H, 1, D] tensor on {cache.device}")
+    return q
 
 
 def sparse_attn_paged_decode_workspace_size(q, cache: PagedCache, g: Graph) -> int:
-    tq = _tensor(q, "q")
+    tq = _tensor(_paged_queries(q, cache), "q")
     return int(_lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(tq), cache._ref,
                                                             g.handle))
 
@@ -482,34 +463,17 @@ def sparse_attn_paged_decode(q, cache: PagedCache, block_table, pos, g: Graph, s
     for a padded one) of the request in row `row` (int32 [N]; default: token
     t's is row t) of block_table (int32 [rows, max_pages]).  Returns (out
     [N, H, 1, D], lse fp32 [N, H])."""
-    tq = _tensor(q, "q")
-    N, H, D, dev = tq.B, tq.H, tq.D, cache._index
-    if q.get_device() != dev:
-        raise ValueError(f"q must be on {cache.device}")
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
-        raise ValueError("block_table must be a CUDA int32 [rows, max_pages] tensor")
-    rows, M = shape = block_table.shape
-    out = torch.empty_like(q) if out is None else out
+    if out is None:
+        out = torch.empty_like(_paged_queries(q, cache))
     if lse is None:
-        lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
-    out_p = _array(out, "out", q.dtype, q.shape, dev)
-    lse_p = _array(lse, "lse", torch.float32, (N, H), dev)
-    table_p = _array(block_table, "block_table", torch.int32, shape, dev)
-    pos_p = _array(pos, "pos", torch.int64, (N,), dev)
-    row_p = None if row is None else _array(row, "row", torch.int32, (N,), dev)
-    if N == 0:
-        return out, lse
-    if workspace is None:
-        size = _lib.sparse_attn_paged_decode_workspace_size(ctypes.byref(tq), cache._ref, g.handle)
-        if size:
-            workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
-    elif workspace.get_device() != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be contiguous on {cache.device}")
-    ws_p, ws_n = (None, 0) if workspace is None else (
-        workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    _call_on(dev, stream, "sparse_attn_paged_decode", _lib.sparse_attn_paged_decode,
-             ctypes.byref(tq), cache._ref, table_p, rows, M, row_p, pos_p, g.handle, float(scale),
-             ctypes.byref(SaTensor(out_p, tq.dtype, N, H, 1, D)), lse_p, ws_p, ws_n)
+        lse = torch.empty(_paged_queries(q, cache).shape[:2], dtype=torch.float32, device=q.device)
+    if workspace is None and q.shape[0]:
+        size = sparse_attn_paged_decode_workspace_size(q, cache, g)
+        workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    status = _paged.decode(q, cache._address, cache._index, block_table, pos, g.handle.value, scale,
+                           row, out, lse, workspace, None if stream is None else _stream(stream))
+    if status != SA_OK:
+        _check(status, "sparse_attn_paged_decode")
     return out, lse
 
 

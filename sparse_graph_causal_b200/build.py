@@ -1,15 +1,19 @@
 """Build libsparse_attn.so in-tree for sm_100a with nvcc (one shared
-library, C ABI, no torch types).  Usage: python -m sparse_graph_causal_b200.build"""
+library, C ABI, no torch types), and beside it _paged, the Python module that
+marshals the paged cache's calls (host C++ on torch's headers).
+Usage: python -m sparse_graph_causal_b200.build"""
 from __future__ import annotations
 
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libsparse_attn.so")
 OBJ = os.path.join(HERE, "_build")
+BIND = os.path.join(HERE, "_paged" + sysconfig.get_config_var("EXT_SUFFIX"))
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -51,7 +55,24 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
+    build_binding(verbose)
     return LIB
+
+
+def build_binding(verbose: bool = False) -> str:
+    src = os.path.join(CSRC, "paged_py.cpp")
+    if _stale(BIND, [src, os.path.join(HERE, "..", "include", "sparse_attn.h")]):
+        from torch.utils.cpp_extension import include_paths, library_paths
+        cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared"]
+        cmd += [f"-I{p}" for p in (*include_paths(), cuda, sysconfig.get_paths()["include"])]
+        cmd += [src, "-o", BIND, *(f"-L{p}" for p in library_paths()), "-lc10", "-lc10_cuda",
+                "-ltorch_cpu", "-ltorch_python", f"-L{HERE}", f"-l:{os.path.basename(LIB)}",
+                "-Wl,-rpath,$ORIGIN"]
+        if verbose:
+            print(" ".join(cmd))
+        subprocess.run(cmd, check=True)
+    return BIND
 
 
 if __name__ == "__main__":
