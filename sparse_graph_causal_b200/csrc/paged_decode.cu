@@ -89,17 +89,17 @@ __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// 4, 8 or 16 bytes of shared memory.
 template <int B>
-__device__ __forceinline__ void load_words(uint32_t *w, const void *p) {
-    if constexpr (B == 16) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
-        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
-    } else if constexpr (B == 8) {
-        const uint2 x = *reinterpret_cast<const uint2 *>(p);
-        w[0] = x.x, w[1] = x.y;
-    } else {
-        w[0] = *reinterpret_cast<const uint32_t *>(p);
-    }
+__device__ __forceinline__ void load_words(uint32_t *w, uint32_t at) {
+    if constexpr (B == 16)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(at));
+    else if constexpr (B == 8)
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(at));
+    else
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(at));
 }
 
 struct E4m3 {
@@ -332,19 +332,29 @@ struct MmaTile {
         }
     }
 
-    // Where 16-byte piece c of row r lies in a staged tile: rows one after the
-    // other, the eight pieces of each 128 bytes permuted so that the lanes that
-    // read together meet different banks (keys: two neighbouring rows, values:
-    // four rows two apart).
-    __device__ __forceinline__ static uint32_t place(int r, int c, int f) {
-        const uint32_t at = r * RB + c * 16;
-        return at ^ (uint32_t)(f << 4);
+    // A staged tile has its rows one after the other, the eight 16-byte pieces
+    // of each 128 bytes permuted so that the lanes that read together meet
+    // different banks: piece p of key row r lies at p ^ 4 (r mod 2) (two
+    // neighbouring rows are read together), of value row r at p ^ 2 (r / 2 mod
+    // 4) (four rows, two apart).  Shorter rows share 128 bytes; there the keys
+    // need no permutation, and 32-byte values have none.  The functions below
+    // split the places into a lane's part and constants.
+    static constexpr bool kKeysXor = RB >= 128, kValuesXor = RB >= 64;
+
+    // Piece i of key 8 x + g for lane (g, t).
+    __device__ __forceinline__ uint32_t key_lane() const {
+        return (g * RB + t * KP) ^ (kKeysXor ? (g & 1) << 6 : 0);
     }
-    __device__ __forceinline__ static uint32_t key_place(int r, int c) {
-        return place(r, c, RB >= 128 ? (r & 1) << 2 : 0);
+    __device__ __forceinline__ static uint32_t key_at(uint32_t lane_part, int x, int i) {
+        return (lane_part ^ ((i & 1) << 6)) + (i >> 1) * 128 + x * 8 * RB;
     }
-    __device__ __forceinline__ static uint32_t value_place(int r, int c) {
-        return place(r, c, RB >= 64 ? ((r >> 1) & 3) << 1 : 0);
+    // Piece i of value row 16 x + 8 (y / 2) + 2 t + y mod 2.
+    __device__ __forceinline__ uint32_t value_lane() const {
+        return KT * RB + 2 * t * RB + ((g * VP) ^ (kValuesXor ? t << 5 : 0));
+    }
+    __device__ __forceinline__ static uint32_t value_at(uint32_t lane_part, int x, int y, int i) {
+        const uint32_t odd = RB == 64 ? (lane_part ^ ((y & 1) << 6)) : lane_part + (y & 1) * RB;
+        return odd + i * 128 + (y >> 1) * 8 * RB + x * 16 * RB;
     }
 
     // Start the copies of a tile: at[] are the offsets of its rows in the
@@ -352,23 +362,30 @@ struct MmaTile {
     __device__ __forceinline__ void copy(const DecodeArgs &a, uint8_t *stage, const int64_t *at,
                                          bool every) const {
         constexpr int L = RB / 16, R = 32 / L;
+        // lane (h, sub): piece sub of row R x + h; R rows are 512 bytes
         const int ln = threadIdx.x & 31, sub = ln % L, h = ln / L;
         const uint32_t dst = smem_addr(stage);
         const uint8_t *k = (const uint8_t *)a.k + sub * 16, *v = (const uint8_t *)a.v + sub * 16;
+        const uint32_t to = h * RB + sub * 16;
+        const uint32_t kd = dst + (to ^ (kKeysXor ? (h & 1) << 6 : 0));
+        const uint32_t vl = to ^ (RB == 128 ? (h >> 1) << 5 : RB == 64 ? ((h >> 1) & 3) << 5 : 0);
+        auto vd = [&](int x) {
+            const int f = RB == 256 ? (x & 3) << 5 : RB == 128 ? (x & 1) << 6 : 0;
+            return dst + KT * RB + (vl ^ f) + x * 512;
+        };
         if (every) {
 #pragma unroll
             for (int x = 0; x < KT / R; ++x) {
                 const int64_t o = at[x * R + h];
-                copy_async16(dst + key_place(x * R + h, sub), k + o);
-                copy_async16(dst + KT * RB + value_place(x * R + h, sub), v + o);
+                copy_async16(kd + x * 512, k + o);
+                copy_async16(vd(x), v + o);
             }
         } else {
 #pragma unroll 1
             for (int x = 0; x < KT / R; ++x) {
                 const int64_t o = at[x * R + h];
-                copy_async<16>(dst + key_place(x * R + h, sub), k + (o < 0 ? 0 : o), o >= 0);
-                copy_async<16>(dst + KT * RB + value_place(x * R + h, sub), v + (o < 0 ? 0 : o),
-                               o >= 0);
+                copy_async<16>(kd + x * 512, k + (o < 0 ? 0 : o), o >= 0);
+                copy_async<16>(vd(x), v + (o < 0 ? 0 : o), o >= 0);
             }
         }
         if constexpr (k8) {
@@ -385,6 +402,8 @@ struct MmaTile {
 
     __device__ __forceinline__ void tile(const uint8_t *stage, uint32_t mask) {
         constexpr int KB = KT / 8;
+        const uint32_t keys = smem_addr(stage) + key_lane();
+        const uint32_t values = smem_addr(stage) + value_lane();
         float s[KB][4];
         const float *scales = reinterpret_cast<const float *>(stage + 2 * KT * RB);
         // scores
@@ -393,10 +412,7 @@ struct MmaTile {
             float s2[2][4] = {};  // two sums side by side: half the chain
             uint32_t w[KN * KP / 4];
 #pragma unroll
-            for (int i = 0; i < KN; ++i) {
-                const int c = (i * 4 + t) * KP;  // byte of the row
-                load_words<KP>(w + i * KP / 4, stage + key_place(x * 8 + g, c / 16) + c % 16);
-            }
+            for (int i = 0; i < KN; ++i) load_words<KP>(w + i * KP / 4, key_at(keys, x, i));
 #pragma unroll
             for (int y = 0; y < KS; ++y) {
                 uint32_t qa[4];
@@ -478,12 +494,7 @@ struct MmaTile {
             for (int i = 0; i < VN; ++i) {
                 uint32_t w[4][VP / 4];
 #pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const int c = (i * 8 + g) * VP;
-                    load_words<VP>(w[y], stage + KT * RB + c % 16 +
-                                             value_place(x * 16 + (y & 2) * 4 + 2 * t + (y & 1),
-                                                         c / 16));
-                }
+                for (int y = 0; y < 4; ++y) load_words<VP>(w[y], value_at(values, x, y, i));
 #pragma unroll
                 for (int z = 0; z < VP / 4; ++z) {
                     uint32_t b0[4], b1[4];
