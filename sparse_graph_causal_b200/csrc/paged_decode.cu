@@ -264,9 +264,15 @@ struct MmaTile {
     static constexpr bool k8 = sizeof(T) == 1;
     static constexpr int D = kD, NQ = 8 * NB;
     static constexpr int RB = D * (int)sizeof(T);          // bytes of a row
+    // Tiles of 8 KB (less for short rows), two or three of them in flight per
+    // warp: 130 to 200 KB an SM, where 45 would cover the latency of an idle
+    // memory.  Twelve warps where their registers suffice (64 bf16 columns: 253
+    // us for 32 rows of 16-32K keys, eight warps 259; 128 8-bit ones spill: 33 us
+    // for a ragged batch of 103 MB, eight warps 30).
     static constexpr int KT = RB == 256 ? 16 : 32;
-    static constexpr int kStages = RB == 32 ? 4 : RB == 128 && NB == 1 ? 2 : 3;
-    static constexpr int kWarps = RB == 256 || NB == 2 || D == 32 ? 8 : 12;
+    static constexpr bool kMany = NB == 1 && D == 64;
+    static constexpr int kStages = RB == 32 ? 4 : RB == 128 && kMany ? 2 : 3;
+    static constexpr int kWarps = kMany ? 12 : 8;
     static constexpr int kOcc = D == 32 && NB == 1 ? 2 : 1;
     static constexpr int KP = RB / 4 < 16 ? RB / 4 : 16, KN = RB / 4 / KP;
     static constexpr int VP = RB / 8 < 16 ? RB / 8 : 16, VN = RB / 8 / VP;
@@ -878,10 +884,13 @@ struct Shares {
 };
 
 // What the start of a row costs a warp (positions, pages and the first copies
-// one after the other, then the merge), in tiles.  The shares count it.
+// one after the other, then its end), in tiles.  The shares count it: 40 ragged
+// rows in 8 bits take 18 us, 24 if it counts 1, 19 if it counts 6; 100 ragged rows
+// of 128 columns 56.5 us, 68 and 57.6.
 constexpr int kRowStart = 3;
-// Fewest tiles worth a warp: below, a share is mostly its own start and merge.
-constexpr int kLeastTiles = 4;
+// Fewest tiles worth a warp: below, a share is mostly its own start (8 rows of
+// 1,600 keys: 10.2 us, 10.7 with 4 or 8).
+constexpr int kLeastTiles = 2;
 
 template <typename Tile>
 __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
