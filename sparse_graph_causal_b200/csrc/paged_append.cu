@@ -103,6 +103,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
     const int64_t base = (int64_t)blockIdx.x * (kThreads * kUnits);
     const int64_t t0 = quotient(base, a.per_token.by);  // token of the block's first piece
     const uint32_t r0 = (uint32_t)(base - t0 * a.per_token.by);
+    chain_begin();
     constexpr int V = kQuant ? 2 : 1;
     uint4 x[2][kUnits][V];
     int64_t token[kUnits];
@@ -180,9 +181,11 @@ template <int L, bool kQuant, int kUnits>
 sa_status launch_units(const AppendArgs &a, cudaStream_t s) {
     const int64_t blocks = (a.units + kThreads * kUnits - 1) / (kThreads * kUnits);
     if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
+    cudaError_t e = cudaSuccess;
     SA_LAUNCH("paged_append", s,
-              paged_append_kernel<L, kQuant, kUnits><<<(unsigned)blocks, kThreads, 0, s>>>(a));
-    SA_CUDA_TRY(cudaGetLastError());
+              e = launch_chained(paged_append_kernel<L, kQuant, kUnits>, dim3((unsigned)blocks),
+                                 kThreads, 0, s, 1, a));
+    SA_CUDA_TRY(e);
     return SA_OK;
 }
 

@@ -852,6 +852,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     using M = Layout<Tile>;
     extern __shared__ __align__(128) uint8_t mem[];
     __shared__ const float *s_part[Tile::kWarps];
+    chain_begin();
     const int U = a.Hkv * a.QB, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
     const int64_t n = blockIdx.x / U;
     const Block b = block_of<Tile::NQ>(a, blockIdx.x % U);
@@ -904,7 +905,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     __shared__ int64_t s_sum[NW];
     __shared__ const float *s_part[NW];  // each warp's ring
     __shared__ int s_inside;             // queries of the row that has the whole CTA, or 0
-    asm volatile("griddepcontrol.launch_dependents;");
+    chain_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t U = (int64_t)a.Hkv * a.QB;
     auto tiles_of = [&](int32_t deg) { return max(1, (deg + KT - 1) / KT); };
@@ -1051,7 +1052,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_decode_join(DecodeArgs a) 
     __shared__ int s_count;
     __shared__ float s_m[R], s_l[R];
     __shared__ float4 s_o[R][C];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    chain_begin();
     if (threadIdx.x < 32) {
         const int lane = threadIdx.x;
         Cut cut = {};
@@ -1165,6 +1166,7 @@ sa_status launch_decode(DecodeArgs &a, const sa_graph_s *graph, const sa_paged_c
     const GraphView g = make_view(graph);
     const int64_t blocks = a.N * a.Hkv * a.QB, longest = longest_row(graph);
     int sms = 0;
+    cudaError_t e = cudaSuccess;
     SA_CUDA_TRY(sa_sm_count(&sms));
     if (is_direct(graph, cache, blocks, sms)) {
         if (blocks > 0x7fffffffLL) return SA_ERR_UNSUPPORTED;
@@ -1177,9 +1179,9 @@ sa_status launch_decode(DecodeArgs &a, const sa_graph_s *graph, const sa_paged_c
         SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_direct<Tile>,
                                   Tile::kWarps * M::kBytes));
         SA_LAUNCH("paged_decode", s,
-                  paged_decode_direct<Tile>
-                  <<<(unsigned)blocks, 32 * (int)nw, (int)nw * M::kBytes, s>>>(a, g));
-        SA_CUDA_TRY(cudaGetLastError());
+                  e = launch_chained(paged_decode_direct<Tile>, dim3((unsigned)blocks),
+                                     32 * (int)nw, nw * M::kBytes, s, 1, a, g));
+        SA_CUDA_TRY(e);
         return SA_OK;
     }
     const Plan p = split_plan<Tile>(sms);
@@ -1187,20 +1189,12 @@ sa_status launch_decode(DecodeArgs &a, const sa_graph_s *graph, const sa_paged_c
     a.cut = (Cut *)(a.part + p.ctas * p.warps * 2 * p.part_floats);
     SA_CUDA_TRY(sa_smem_optin((const void *)paged_decode_split<Tile>, Tile::kWarps * M::kBytes));
     SA_LAUNCH("paged_decode", s,
-              paged_decode_split<Tile>
-              <<<(unsigned)p.ctas, 32 * Tile::kWarps, Tile::kWarps * M::kBytes, s>>>(a, g));
-    SA_CUDA_TRY(cudaGetLastError());
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
-    cfg.gridDim = dim3((unsigned)p.ctas, (unsigned)(a.G < Tile::NQ ? a.G : Tile::NQ));
-    cfg.blockDim = dim3(kJoinThreads);
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    cudaError_t e = cudaSuccess;
-    SA_LAUNCH("paged_decode_join", s, e = cudaLaunchKernelEx(&cfg, paged_decode_join<Tile>, a));
+              e = launch_chained(paged_decode_split<Tile>, dim3((unsigned)p.ctas),
+                                 32 * Tile::kWarps, Tile::kWarps * M::kBytes, s, 1, a, g));
+    SA_CUDA_TRY(e);
+    const dim3 grid((unsigned)p.ctas, (unsigned)(a.G < Tile::NQ ? a.G : Tile::NQ));
+    SA_LAUNCH("paged_decode_join", s,
+              e = launch_chained(paged_decode_join<Tile>, grid, kJoinThreads, 0, s, 1, a));
     SA_CUDA_TRY(e);
     return SA_OK;
 }

@@ -81,6 +81,7 @@ constexpr int kRefused = -1;
 // NT threads; PER requests each (consecutive ones), kept in registers.
 template <int NT, int PER>
 __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
+    chain_begin();
     const sa_paged_step &a = args.s;
     constexpr int NW = NT / 32;
     extern __shared__ int32_t smem[];
@@ -277,20 +278,11 @@ sa_status launch_plan(const PlanArgs &p, cudaStream_t s) {
     const void *fn = (const void *)paged_plan_kernel<NT, PER>;
     // the opt-in holds for the largest B of this variant
     SA_CUDA_TRY(sa_smem_optin(fn, 4 * 4 * PER * NT));
-    cudaLaunchConfig_t cfg = {};
-    cudaLaunchAttribute attr[1];
     const int ncta = p.s.capacity > 2048 ? 8 : 1;
-    cfg.gridDim = dim3(ncta);
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = 4 * (size_t)(p.size + 2 * p.s.B);
-    cfg.stream = s;
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = ncta;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
     cudaError_t e = cudaSuccess;
-    SA_LAUNCH("paged_plan", s, e = cudaLaunchKernelEx(&cfg, paged_plan_kernel<NT, PER>, p));
+    SA_LAUNCH("paged_plan", s,
+              e = launch_chained(paged_plan_kernel<NT, PER>, dim3(ncta), NT,
+                                 4 * (size_t)(p.size + 2 * p.s.B), s, ncta, p));
     SA_CUDA_TRY(e);
     return SA_OK;
 }
