@@ -36,13 +36,16 @@ struct AppendArgs {
     int *err;
 };
 
-// Correctly rounded x / s for 2^-60 <= s <= 2^60 and quotients above 2^-40
-// (smaller ones are off by less than 2^-60): r is 1 / s rounded to nearest,
-// the first correction brings the quotient within an ulp, and by P. Markstein's
-// theorem (IBM J. Res. Dev. 34, 1990) the second makes it the nearest.
+// x / s, rounded to nearest but for quotients within 2^-45 of a border between
+// two fp32 numbers, for 2^-60 <= s <= 2^60 (and x not far below; what is, has code
+// 0): r is 1 / s rounded to nearest, x r is within 2^-23 of the quotient, and the
+// correction by its remainder, itself off by 2^-23 of that, leaves 2^-45.  The
+// quotients here are of bf16 numbers by 1 / 448 of one: none lies that close to a
+// border that would change its code (checked over all pairs of significands), and
+// amax / 448 is a seventh of a whole number of ulps away from every border, so that
+// scales and codes are those of IEEE division.
 __device__ __forceinline__ float quotient_rn(float x, float s, float r) {
-    float q = x * r;
-    q = fmaf(fmaf(-q, s, x), r, q);
+    const float q = x * r;
     return fmaf(fmaf(-q, s, x), r, q);
 }
 

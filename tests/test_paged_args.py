@@ -170,6 +170,47 @@ def test_e4m3_statement_agrees_with_the_type():
     assert np.array_equal(paged_ref.e4m3_round(y.astype(np.float64)), want)
 
 
+def _rounded(num, den):
+    """num / den > 0 to 24 significant bits, halves to even: (significand, exponent)."""
+    e = num.bit_length() - den.bit_length() - 24
+    while True:
+        n, d = (num << -e, den) if e < 0 else (num, den << e)
+        q, r = divmod(n, d)
+        if 1 << 23 <= q < 1 << 24:
+            q += 2 * r > d or (2 * r == d and q & 1)
+            return (q, e) if q < 1 << 24 else (q >> 1, e + 1)
+        e += 1 if q >> 24 else -1
+
+
+def _code(m, e):
+    """m * 2^e rounded to e4m3, as a multiple of 2^-9."""
+    step = max(m.bit_length() + e - 1, -6) - 3
+    shift = step - e
+    if shift > 0:
+        q, r, half = m >> shift, m & ((1 << shift) - 1), 1 << (shift - 1)
+        m = q + (r > half or (r == half and q & 1))
+    else:
+        m <<= -shift
+    return m << (step + 9)
+
+
+def test_quotients_off_by_2_to_the_minus_45_have_the_same_codes():
+    """The rounding of 8-bit rows divides with one correction step, whose result is the rounding
+    of a quotient off by at most 2^-45: over all significands of a bf16 value and of its row's
+    largest magnitude, the code is that of the correctly rounded quotient, and so is the scale."""
+    lo, hi = (1 << 45) - 1, (1 << 45) + 1
+    for A in range(128, 256):
+        S, e = _rounded(A, 448)
+        assert {_rounded(A * lo, 448 << 45), _rounded(A * hi, 448 << 45)} == {(S, e)}
+        for X in range(128, 256):
+            for j in range(24):                      # x = X 2^-j, amax = A
+                if X <= A << j:
+                    num, den = X << -e, S << j       # e < 0
+                    code = _code(*_rounded(num, den))
+                    assert _code(*_rounded(num * lo, den << 45)) == code
+                    assert _code(*_rounded(num * hi, den << 45)) == code
+
+
 def test_attend_statement_by_hand():
     q = np.array([[1.0, 0.0]])
     k = np.array([[0.0, 5.0], [np.log(3.0), 1.0]])
