@@ -23,6 +23,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "paged_common.cuh"
 #include "sa_internal.cuh"
 
@@ -31,6 +33,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kRun = 4;  // tokens of a thread at a time
 
 // Sums that stop at the largest value (they are compared with stack sizes).
 __device__ __forceinline__ uint32_t add_sat(uint32_t a, uint32_t b) {
@@ -226,7 +229,6 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
 
     // tokens: kRun of a thread, NT apart, so that their loads overlap and
     // neighbours store together
-    constexpr int kRun = 4;
     const int32_t capacity = (int32_t)a.capacity;
     for (int32_t t0 = rank * NT * kRun; t0 < capacity; t0 += ncta * NT * kRun) {
         int32_t page[kRun], row[kRun], pos[kRun];
@@ -273,12 +275,46 @@ __global__ void __launch_bounds__(NT) paged_plan_kernel(const PlanArgs args) {
     }
 }
 
+// Whether the device takes clusters of 16 of this kernel (beyond the portable
+// eight), asked once per kernel and device.
+template <int NT, int PER>
+bool takes_sixteen(size_t smem) {
+    static std::atomic<int8_t> known[64];  // 0: not asked, 1: no, 2: yes
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+    int8_t k = known[dev].load(std::memory_order_relaxed);
+    if (k == 0) {
+        const auto fn = paged_plan_kernel<NT, PER>;
+        int clusters = 0;
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        cfg.gridDim = dim3(16);
+        cfg.blockDim = dim3(NT);
+        cfg.dynamicSmemBytes = smem;
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 16;
+        attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        const bool ok =
+            cudaFuncSetAttribute((const void *)fn, cudaFuncAttributeNonPortableClusterSizeAllowed,
+                                 1) == cudaSuccess &&
+            cudaOccupancyMaxActiveClusters(&clusters, fn, &cfg) == cudaSuccess && clusters > 0;
+        if (!ok) cudaGetLastError();  // an answer, not a failure
+        k = ok ? 2 : 1;
+        known[dev].store(k, std::memory_order_relaxed);
+    }
+    return k == 2;
+}
+
 template <int NT, int PER>
 sa_status launch_plan(const PlanArgs &p, cudaStream_t s) {
     const void *fn = (const void *)paged_plan_kernel<NT, PER>;
     // the opt-in holds for the largest B of this variant
     SA_CUDA_TRY(sa_smem_optin(fn, 4 * 4 * PER * NT));
-    const int ncta = p.s.capacity > 2048 ? 8 : 1;
+    // as many CTAs as give each one turn of tokens
+    int ncta = p.s.capacity > 2048 ? 8 : 1;
+    if (p.s.capacity > 8 * NT * kRun && takes_sixteen<NT, PER>(4 * 4 * PER * NT)) ncta = 16;
     cudaError_t e = cudaSuccess;
     SA_LAUNCH("paged_plan", s,
               e = launch_chained(paged_plan_kernel<NT, PER>, dim3(ncta), NT,

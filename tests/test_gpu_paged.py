@@ -80,7 +80,7 @@ def _check_plan(got, want):
     (1, 1, 1, 1.0, 1), (1, 5, 16, 1.0, 200), (3, 4, 7, 1.0, 100), (64, 12, 16, 0.5, 5000),
     (300, 6, 17, 0.8, 20000), (1024, 3, 8, 0.9, 9000), (1025, 3, 8, 0.9, 9001),
     (2500, 2, 32, 0.6, 60000), (8192, 2, 4, 1.0, 33333), (40, 5, 24, 0.0, 2048),
-    (40, 5, 24, 1.0, 37),
+    (40, 5, 24, 1.0, 37), (900, 4, 16, 0.7, 50001), (2000, 3, 16, 0.7, 70000),
 ])
 def test_plan(sa, B, M, page, enough, capacity, in_place):
     rng = np.random.default_rng(B * 1000 + M + page)
