@@ -220,9 +220,10 @@ __device__ __forceinline__ Token token_of(const DecodeArgs &a, const GraphView &
 // apart, meet different banks.
 template <int NQ, int D>
 struct Part {
-    static constexpr int kFloats = NQ * (D + 2);
+    static constexpr int kHead = NQ < 2 ? 4 : 2 * NQ;  // (16-byte steps)
+    static constexpr int kFloats = kHead + NQ * D;
     __device__ __forceinline__ static int place(int q, int four) {
-        return 2 * NQ + q * D + 4 * (four ^ ((((four >> 3) << 1) | (q & 1)) & 7));
+        return kHead + q * D + 4 * (four ^ ((((four >> 3) << 1) | (q & 1)) & 7));
     }
 };
 
@@ -563,6 +564,8 @@ struct MmaTile {
 
 // ------------------------------------------------------------ fp32 tiles
 
+// The queries of a group are a constant (1, 2, 4, 8 or 16, the rest zero), so that
+// their sums and shuffles run side by side.
 template <int kD, int kNQ>
 struct FmaTile {
     using Out = float;
@@ -579,19 +582,21 @@ struct FmaTile {
     static constexpr int KE = KT / KG;    // keys of a lane
     static_assert(KE == 8, "two groups of four");
 
-    int lane, gq;
+    int lane;
     float *qs, *ps;
     float m[NQ], l[NQ];
     float4 acc[NQ];
 
     __device__ __forceinline__ void begin(const DecodeArgs &a, void *own, int64_t n, int64_t h0,
                                           int queries) {
-        lane = threadIdx.x & 31, gq = queries;
+        lane = threadIdx.x & 31;
         qs = (float *)own;
         ps = qs + NQ * D;
         __syncwarp();
-        for (int x = lane; x < gq * C; x += 32) {
-            float4 q = reinterpret_cast<const float4 *>((const float *)a.q + (n * a.H + h0) * D)[x];
+        for (int x = lane; x < NQ * C; x += 32) {
+            float4 q = make_float4(0.f, 0.f, 0.f, 0.f);  // (the queries beyond the group)
+            if (x < queries * C)
+                q = reinterpret_cast<const float4 *>((const float *)a.q + (n * a.H + h0) * D)[x];
             q.x *= a.scale2, q.y *= a.scale2, q.z *= a.scale2, q.w *= a.scale2;
             reinterpret_cast<float4 *>(qs)[x] = q;
         }
@@ -632,31 +637,29 @@ struct FmaTile {
             const float4 k =
                 *reinterpret_cast<const float4 *>(stage + key * RB + ((c ^ (key & 7)) << 4));
 #pragma unroll
-            for (int x = 0; x < NQ; ++x)
-                if (x < gq) {
-                    const float4 q = reinterpret_cast<const float4 *>(qs)[x * C + c];
-                    s[x] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[x]))));
-                }
+            for (int x = 0; x < NQ; ++x) {
+                const float4 q = reinterpret_cast<const float4 *>(qs)[x * C + c];
+                s[x] = fmaf(q.x, k.x, fmaf(q.y, k.y, fmaf(q.z, k.z, fmaf(q.w, k.w, s[x]))));
+            }
         }
         const bool on = (mask >> key) & 1;
 #pragma unroll
-        for (int x = 0; x < NQ; ++x)
-            if (x < gq) {
-                float z = s[x];
+        for (int x = 0; x < NQ; ++x) {
+            float z = s[x];
 #pragma unroll
-                for (int o = KT; o < 32; o <<= 1) z += __shfl_xor_sync(kFull, z, o);
-                if (!on) z = -INFINITY;
-                float top = z;
+            for (int o = KT; o < 32; o <<= 1) z += __shfl_xor_sync(kFull, z, o);
+            if (!on) z = -INFINITY;
+            float top = z;
 #pragma unroll
-                for (int o = KT / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
-                top = fmaxf(top, m[x]);
-                const float base = finite_base(top), fall = ex2(m[x] - base);
-                const float p = ex2(z - base);
-                m[x] = top;
-                l[x] = l[x] * fall + p;
-                acc[x].x *= fall, acc[x].y *= fall, acc[x].z *= fall, acc[x].w *= fall;
-                if (part == 0) ps[x * KT + key] = p;
-            }
+            for (int o = KT / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
+            top = fmaxf(top, m[x]);
+            const float base = finite_base(top), fall = ex2(m[x] - base);
+            const float p = ex2(z - base);
+            m[x] = top;
+            l[x] = l[x] * fall + p;
+            acc[x].x *= fall, acc[x].y *= fall, acc[x].z *= fall, acc[x].w *= fall;
+            if (part == 0) ps[x * KT + key] = p;
+        }
         __syncwarp();
         const int c = lane % C, kg = lane / C;
 #pragma unroll
@@ -669,19 +672,17 @@ struct FmaTile {
                                                          ((c ^ (j & 7)) << 4));
             }
 #pragma unroll
-            for (int x = 0; x < NQ; ++x)
-                if (x < gq) {
-                    const float4 p =
-                        *reinterpret_cast<const float4 *>(ps + x * KT + kg * KE + k0);
-                    const float pp[4] = {p.x, p.y, p.z, p.w};
+            for (int x = 0; x < NQ; ++x) {
+                const float4 p = *reinterpret_cast<const float4 *>(ps + x * KT + kg * KE + k0);
+                const float pp[4] = {p.x, p.y, p.z, p.w};
 #pragma unroll
-                    for (int y = 0; y < 4; ++y) {
-                        acc[x].x = fmaf(pp[y], v[y].x, acc[x].x);
-                        acc[x].y = fmaf(pp[y], v[y].y, acc[x].y);
-                        acc[x].z = fmaf(pp[y], v[y].z, acc[x].z);
-                        acc[x].w = fmaf(pp[y], v[y].w, acc[x].w);
-                    }
+                for (int y = 0; y < 4; ++y) {
+                    acc[x].x = fmaf(pp[y], v[y].x, acc[x].x);
+                    acc[x].y = fmaf(pp[y], v[y].y, acc[x].y);
+                    acc[x].z = fmaf(pp[y], v[y].z, acc[x].z);
+                    acc[x].w = fmaf(pp[y], v[y].w, acc[x].w);
                 }
+            }
         }
         __syncwarp();
     }
@@ -1006,7 +1007,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
                 } else if (!inside) {
                     float4 *part =
                         reinterpret_cast<float4 *>(a.part + (W * 2 + (goes_on ? 0 : 1)) * PF);
-                    for (int i = lane; i < (2 * Tile::NQ + b.gq * D) / 4; i += 32)
+                    for (int i = lane; i < (M::P::kHead + b.gq * D) / 4; i += 32)
                         part[i] = reinterpret_cast<const float4 *>(own)[i];
                     if (!goes_on) {
                         const int64_t last = shares.of(row1 - 1), cta = quotient(last, nw);
@@ -1139,7 +1140,9 @@ auto with_tile(const sa_paged_cache &c, int64_t G, F f)
             return G > 8 ? f((MmaTile<E4m3, d, 2> *)0) : f((MmaTile<E4m3, d, 1> *)0); \
         return G > 8   ? f((FmaTile<d, 16> *)0)                                       \
                : G > 4 ? f((FmaTile<d, 8> *)0)                                        \
-                       : f((FmaTile<d, 4> *)0);                                       \
+               : G > 2 ? f((FmaTile<d, 4> *)0)                                        \
+               : G > 1 ? f((FmaTile<d, 2> *)0)                                        \
+                       : f((FmaTile<d, 1> *)0);                                       \
     }
     SA_PAGED_TILE(32)
     SA_PAGED_TILE(64)
