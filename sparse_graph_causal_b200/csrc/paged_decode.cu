@@ -453,15 +453,28 @@ struct MmaTile {
                 for (int y = 0; y < 2; ++y) {
                     const int key = x * 8 + 2 * t + y;
                     float z = s[x][2 * b + y] * unit[b];
-                    if constexpr (k8) z *= scales[key];
-                    if (mask != all && !((mask >> key) & 1)) z = -INFINITY;
-                    s[x][2 * b + y] = z;
-                    top = fmaxf(top, z);
                     if constexpr (k8) {
+                        z *= scales[key];
                         lv[x][y] = lg2(fabsf(scales[KT + key]));
-                        if (mask != all && !((mask >> key) & 1)) lv[x][y] = 0.f;
-                        topw = fmaxf(topw, z + lv[x][y]);
                     }
+                    s[x][2 * b + y] = z;
+                }
+            if (mask != all) {
+#pragma unroll
+                for (int x = 0; x < KB; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        if (!((mask >> (x * 8 + 2 * t + y)) & 1)) {
+                            s[x][2 * b + y] = -INFINITY;
+                            if constexpr (k8) lv[x][y] = 0.f;
+                        }
+            }
+#pragma unroll
+            for (int x = 0; x < KB; ++x)
+#pragma unroll
+                for (int y = 0; y < 2; ++y) {
+                    top = fmaxf(top, s[x][2 * b + y]);
+                    if constexpr (k8) topw = fmaxf(topw, s[x][2 * b + y] + lv[x][y]);
                 }
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 1));
             top = fmaxf(top, __shfl_xor_sync(kFull, top, 2));
