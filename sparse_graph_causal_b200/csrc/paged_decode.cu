@@ -1121,13 +1121,14 @@ int64_t longest_row(const sa_graph_s *g) {
 }
 
 // Rows that the direct way takes, by the bytes of keys and values of the longest.
-// Below kDirectBytes it is the faster one whatever the batch (8 rows of 128 KB:
-// 8.3 us against 12.5, of 512 KB: 14.4 and 14.5; 2,048 rows of 128 KB: 61 and 71,
-// of 384 KB: 158 and 156).  Rows that nearly all have the window's length and
-// fill the SMs in one go are better left whole up to kDirectUniform (128 rows of
-// 1 MB: 27 against 35 us, of 2 MB: 46 against 55; 160 rows of 512 KB: 27
-// against 25, for they take two goes).
-constexpr int64_t kDirectBytes = 384 << 10, kDirectUniform = 2 << 20;
+// Up to kDirectBytes it is the faster one for nearly every batch (direct and split,
+// us: 8 rows of 128 KB 5.4, 9.0; of 384 KB 9.9, 10.2; of 512 KB 12.1, 10.5; 2,048
+// rows of 128 KB 58, 56, of 384 KB 156, 139), up to kDirectSome where the rows are
+// half to four times the SMs (160 rows of 768 KB 30, 32; 512 rows 66, 77; 80 rows
+// of 512 KB 20, 21), and up to kDirectUniform where rows that nearly all have the
+// window's length fill the SMs in one go (128 rows of 2 MB: 44, 54; of 8-bit rows
+// 58, 60).
+constexpr int64_t kDirectBytes = 384 << 10, kDirectSome = 768 << 10, kDirectUniform = 2 << 20;
 
 int64_t longest_bytes(const sa_graph_s *g, const sa_paged_cache &c) {
     return longest_row(g) * 2 * c.D * (c.dtype == SA_FP32 ? 4 : c.dtype == SA_BF16 ? 2 : 1);
@@ -1136,6 +1137,7 @@ int64_t longest_bytes(const sa_graph_s *g, const sa_paged_cache &c) {
 bool is_direct(const sa_graph_s *g, const sa_paged_cache &c, int64_t rows, int sms) {
     const int64_t bytes = longest_bytes(g, c);
     if (bytes <= kDirectBytes) return true;
+    if (bytes <= kDirectSome && 2 * rows >= sms && rows <= 4 * sms) return true;
     const bool uniform = g->kind == 0 && g->W <= g->T / 4;
     return bytes <= kDirectUniform && uniform && rows <= sms && 4 * rows >= 3 * sms;
 }
