@@ -921,7 +921,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     constexpr int PF = M::P::kFloats, D = Tile::D;
     using Out = typename Tile::Out;
     extern __shared__ __align__(128) uint8_t mem[];
-    __shared__ int64_t s_start[NT + 1];  // row tiles before each thread's rows
+    __shared__ int64_t s_start[NT + 1];  // what the rows before each thread's cost
     __shared__ int64_t s_sum[NW];
     __shared__ const float *s_part[NW];  // each warp's ring
     __shared__ int s_inside;             // queries of the row that has the whole CTA, or 0
@@ -931,7 +931,7 @@ __global__ void __launch_bounds__(32 * Tile::kWarps, Tile::kOcc)
     auto tiles_of = [&](int32_t deg) { return max(1, (deg + KT - 1) / KT); };
     auto cost_of = [&](int32_t deg) { return tiles_of(deg) + kRowStart; };
 
-    // how many tiles there are, and where each run of rows begins
+    // what all rows cost, and where each run of rows begins
     const int64_t per = (a.N + NT - 1) / NT;
     {
         int64_t own = 0;
