@@ -699,6 +699,60 @@ def test_captured_step_advances(sa, W, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("W", [32, 6000])
+def test_calls_in_a_row_wait_for_one_another(sa, W, dtype):
+    """Each call is launched while the one before it runs.  Every step reads what the step before
+    wrote (lengths, pages, cache rows, and its outputs as the next keys, values and queries): the
+    same bits as with a synchronisation after every call, on the current stream and on a given one."""
+    B, H, Hkv, D, page, M, steps = 4, 4, 2, 64, 16, 400, 60
+    g = sa.sparse_attn_graph_build_structured(M * page, W, list(range(13)))
+    qt = torch.float32 if dtype == "fp32" else torch.bfloat16
+    ones = torch.ones(B, dtype=torch.int32, device="cuda")
+
+    def run(after, stream):
+        s = _server(sa, dtype, B=B, M=M, page=page)
+        gen = torch.Generator("cuda")
+        gen.manual_seed(4)
+        lens = torch.tensor([3000, 17, 5900, 1], dtype=torch.int32, device="cuda")
+        first, batch = sa.PagedBatch(B, 9000), sa.PagedBatch(B, B)
+        x = torch.empty((9000, 2 * Hkv, D), device="cuda").normal_(generator=gen).to(qt)
+        q = torch.empty((B, H, 1, D), device="cuda").normal_(generator=gen).to(qt)
+        torch.cuda.synchronize()
+        n = sa.sparse_attn_paged_decode_workspace_size(q, s["cache"], g)
+        ws = torch.empty(max(n, 1), dtype=torch.uint8, device="cuda")
+        outs = []
+        with torch.cuda.stream(stream or torch.cuda.current_stream()):
+            given = dict(stream=stream) if stream else {}
+            sa.sparse_attn_paged_plan(s["length"], lens, s["table"], s["stack"], s["count"], page,
+                                      first, **given)
+            after()
+            sa.sparse_attn_paged_append(x[:, :Hkv], x[:, Hkv:], s["cache"], first.slot, **given)
+            after()
+            for _ in range(steps):
+                sa.sparse_attn_paged_plan(s["length"], ones, s["table"], s["stack"], s["count"],
+                                          page, batch, **given)
+                after()
+                rows = q[:, :, 0]
+                sa.sparse_attn_paged_append(rows[:, :Hkv], rows[:, Hkv:], s["cache"], batch.slot,
+                                            **given)
+                after()
+                out, lse = sa.sparse_attn_paged_decode(q, s["cache"], s["table"], batch.pos, g, 0.2,
+                                                       row=batch.row, workspace=ws, **given)
+                after()
+                outs.append((out, lse))
+                q = torch.roll(out, 1, 3) + q
+        torch.cuda.synchronize()
+        return outs
+
+    want = run(torch.cuda.synchronize, None)
+    for stream in (None, torch.cuda.Stream()):
+        for (o, l), (o2, l2) in zip(want, run(lambda: None, stream)):
+            assert torch.equal(o, o2) and torch.equal(l, l2)
+    assert torch.isfinite(want[-1][1]).all()
+    sa.sparse_attn_check_device()
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
 def test_captured_decode_of_long_rows(sa, dtype):
     """Rows cut over the GPU in a captured graph: replays follow the positions in place."""
     c = Case([20000, 15000, 77], 8, 2, 64, 16, dtype, 20001, 20001)
