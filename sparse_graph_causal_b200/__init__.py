@@ -6,9 +6,15 @@ only marshals torch tensors (device memory) and the current CUDA stream into
 the C ABI declared in include/sparse_attn.h, under the same names.  There is
 no CPU fallback: the library is loaded on first use and every call raises
 when it is not built or when it reports an error.
+
+A call runs on the current stream or on the one given as `stream`
+(torch.cuda.Stream or a handle); the tensors that it makes belong to that
+stream, as if made under torch.cuda.stream(stream): another stream waits for
+the call before it reads them, and record_stream keeps them for its own use.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -153,6 +159,19 @@ def _stream(stream):
     return int(stream)
 
 
+def _made_on(stream, device):
+    """Where a call makes the tensors that it was not given.  The allocator
+    hands freed memory on in the order of the stream that it was made on: that
+    has to be the stream of the call's kernels, or a workspace, free as soon as
+    the call returns, would be taken and overwritten while they use it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):  # (1: the legacy default stream's other handle)
+        handle = int(stream)
+        stream = torch.cuda.ExternalStream(0 if handle == 1 else handle, device=device)
+    return torch.cuda.stream(stream)
+
+
 def _tensor(t: torch.Tensor, name: str) -> SaTensor:
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -234,10 +253,11 @@ def sparse_attn_graph_export(g: Graph, stream=None, device=None):
     as new CUDA tensors."""
     nnz, _ = sparse_attn_graph_nnz(g)
     dev = device or torch.device("cuda", torch.cuda.current_device())
-    rp = torch.empty(g.T + 1, dtype=torch.int64, device=dev)
-    ci = torch.empty(nnz, dtype=torch.int32, device=dev)
-    rrp = torch.empty(g.T + 1, dtype=torch.int64, device=dev)
-    rci = torch.empty(nnz, dtype=torch.int32, device=dev)
+    with _made_on(stream, dev):
+        rp = torch.empty(g.T + 1, dtype=torch.int64, device=dev)
+        ci = torch.empty(nnz, dtype=torch.int32, device=dev)
+        rrp = torch.empty(g.T + 1, dtype=torch.int64, device=dev)
+        rci = torch.empty(nnz, dtype=torch.int32, device=dev)
     _check(_lib.sparse_attn_graph_export(g.handle, rp.data_ptr(), ci.data_ptr() if nnz else None,
                                          rrp.data_ptr(), rci.data_ptr() if nnz else None,
                                          _stream(stream)),
@@ -256,10 +276,10 @@ def sparse_attn_graph_destroy(g: Graph):
 def sparse_attn_fwd(q, k, v, g: Graph, scale: float, out=None, lse=None, stream=None):
     """Returns (out [B,H,T,D] in q's dtype, lse fp32 [B,H,T])."""
     B, H, T, D = q.shape
-    if out is None:
-        out = torch.empty_like(q)
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
+    with _made_on(stream, q.device):
+        out = torch.empty_like(q) if out is None else out
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=q.device)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H, T):
         raise ValueError("lse must be a contiguous fp32 [B, H, T] tensor")
     tq, tk, tv, to = (_tensor(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out")))
@@ -277,12 +297,13 @@ def sparse_attn_bwd_workspace_size(q, g: Graph) -> int:
 def sparse_attn_bwd(q, k, v, out, lse, dout, g: Graph, scale: float, dq=None, dk=None, dv=None,
                     workspace=None, stream=None):
     """Returns (dq, dk, dv)."""
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
     ws_bytes = sparse_attn_bwd_workspace_size(q, g)
-    if workspace is None:
-        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
+    with _made_on(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=q.device)
     if lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32")
     ts = [_tensor(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout"),
@@ -303,9 +324,10 @@ def sparse_attn_bwd_noalloc(q, k, v, out, lse, dout, g: Graph, scale: float, dq=
     the GPU race on it.  Output tensors passed in are written, not
     allocated; the defaults below allocate them here, in Python, for
     convenience."""
-    dq = torch.empty_like(q) if dq is None else dq
-    dk = torch.empty_like(k) if dk is None else dk
-    dv = torch.empty_like(v) if dv is None else dv
+    with _made_on(stream, q.device):
+        dq = torch.empty_like(q) if dq is None else dq
+        dk = torch.empty_like(k) if dk is None else dk
+        dv = torch.empty_like(v) if dv is None else dv
     if lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32")
     ts = [_tensor(x, n) for x, n in ((q, "q"), (k, "k"), (v, "v"), (out, "out"), (dout, "dout"),
@@ -328,9 +350,10 @@ def sparse_attn_decode(q, k_cache, v_cache, pos, g: Graph, scale: float, out=Non
     query's own key/value already at cache row pos[b]).  Returns (out
     [B, H, 1, D], lse fp32 [B, H])."""
     B, H, _, D = q.shape
-    out = torch.empty_like(q) if out is None else out
-    if lse is None:
-        lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
+    with _made_on(stream, q.device):
+        out = torch.empty_like(q) if out is None else out
+        if lse is None:
+            lse = torch.empty((B, H), dtype=torch.float32, device=q.device)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H):
         raise ValueError("lse must be a contiguous fp32 [B, H] tensor")
     if pos.dtype != torch.int64 or not pos.is_cuda or pos.numel() != B:
@@ -463,13 +486,15 @@ def sparse_attn_paged_decode(q, cache: PagedCache, block_table, pos, g: Graph, s
     for a padded one) of the request in row `row` (int32 [N]; default: token
     t's is row t) of block_table (int32 [rows, max_pages]).  Returns (out
     [N, H, 1, D], lse fp32 [N, H])."""
-    if out is None:
-        out = torch.empty_like(_paged_queries(q, cache))
-    if lse is None:
-        lse = torch.empty(_paged_queries(q, cache).shape[:2], dtype=torch.float32, device=q.device)
-    if workspace is None and q.shape[0]:
-        size = sparse_attn_paged_decode_workspace_size(q, cache, g)
-        workspace = torch.empty(size, dtype=torch.uint8, device=q.device) if size else None
+    if out is None or lse is None or workspace is None:
+        N, H = _paged_queries(q, cache).shape[:2]
+        size = sparse_attn_paged_decode_workspace_size(q, cache, g) if N and workspace is None else 0
+        with _made_on(stream, q.device):
+            out = torch.empty_like(q) if out is None else out
+            if lse is None:
+                lse = torch.empty((N, H), dtype=torch.float32, device=q.device)
+            if size:
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
     status = _paged.decode(q, cache._address, cache._index, block_table, pos, g.handle.value, scale,
                            row, out, lse, workspace, None if stream is None else _stream(stream))
     if status != SA_OK:
@@ -492,9 +517,10 @@ def sparse_attn_dist_fwd(a, c, v, g: Graph, scale: float, out=None, lse=None, st
     """s_ij = -scale |a_i - c_j|^2 over the graph's lists; a, c fp32
     [B, H, T, 3].  Returns (out [B, H, T, D] in v's dtype, lse fp32 [B, H, T])."""
     B, H, T, D = v.shape
-    out = torch.empty_like(v) if out is None else out
-    if lse is None:
-        lse = torch.empty((B, H, T), dtype=torch.float32, device=v.device)
+    with _made_on(stream, v.device):
+        out = torch.empty_like(v) if out is None else out
+        if lse is None:
+            lse = torch.empty((B, H, T), dtype=torch.float32, device=v.device)
     if lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != (B, H, T):
         raise ValueError("lse must be a contiguous fp32 [B, H, T] tensor")
     ta, tc = _coords(a, "a"), _coords(c, "c")
@@ -514,12 +540,13 @@ def sparse_attn_dist_bwd_workspace_size(v, g: Graph) -> int:
 def sparse_attn_dist_bwd(a, c, v, out, lse, dout, g: Graph, scale: float, da=None, dc=None,
                          dv=None, workspace=None, stream=None):
     """Returns (da, dc, dv)."""
-    da = torch.empty_like(a) if da is None else da
-    dc = torch.empty_like(c) if dc is None else dc
-    dv = torch.empty_like(v) if dv is None else dv
-    if workspace is None:
-        workspace = torch.empty(sparse_attn_dist_bwd_workspace_size(v, g), dtype=torch.uint8,
-                                device=v.device)
+    ws_bytes = 0 if workspace is not None else sparse_attn_dist_bwd_workspace_size(v, g)
+    with _made_on(stream, v.device):
+        da = torch.empty_like(a) if da is None else da
+        dc = torch.empty_like(c) if dc is None else dc
+        dv = torch.empty_like(v) if dv is None else dv
+        if workspace is None:
+            workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=v.device)
     if lse.dtype != torch.float32 or not lse.is_contiguous():
         raise ValueError("lse must be contiguous fp32")
     ta, tc, tda, tdc = _coords(a, "a"), _coords(c, "c"), _coords(da, "da"), _coords(dc, "dc")
