@@ -300,7 +300,9 @@ size_t sparse_attn_paged_decode_workspace_size(const sa_tensor *q, const sa_page
  * min(g's T, max_pages * page_size), or row[t] is outside [0, rows).  A key
  * whose block-table entry is outside [0, n_pages) is left out of the softmax
  * and flagged.  Cache rows outside N(pos[t]) are never used, whatever they
- * hold.  A row whose scores are all -inf gives out = 0, lse = -inf.  lse:
+ * hold.  A row whose scores are all -inf gives out = 0, lse = -inf.  Sums are
+ * held in fp32 and divided at the end, the largest probability of a row as
+ * 1: sum_j p_j |v_j| has to stay below fp32's largest value, 2^128.  lse:
  * fp32 [N, H].  Long rows are cut into shares for the whole GPU and joined
  * by a second kernel in a fixed order: results do not change from run to
  * run.  workspace: caller-owned, 256-byte aligned, contents don't matter

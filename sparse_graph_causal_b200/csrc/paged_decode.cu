@@ -152,6 +152,13 @@ __device__ __forceinline__ void split16(float p0, float p1, uint32_t &hi, uint32
     lo = half_bits(__floats2half2_rn(p0 - f.x, p1 - f.y));
 }
 
+// log2 of numbers down to fp32's smallest (the ftz form takes those below 2^-126 for zero).
+__device__ __forceinline__ float lg2_any(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 __device__ __forceinline__ float finite_base(float m) { return m == -INFINITY ? 0.f : m; }
 
 // --------------------------------------------------------------- arguments
@@ -410,12 +417,22 @@ struct MmaTile {
         }
     }
 
-    __device__ __forceinline__ void tile(const uint8_t *stage, uint32_t mask) {
+    __device__ __forceinline__ void tile(uint8_t *stage, uint32_t mask) {
         constexpr int KB = KT / 8;
         const uint32_t keys = smem_addr(stage) + key_lane();
         const uint32_t values = smem_addr(stage) + value_lane();
         float s[KB][4];
-        const float *scales = reinterpret_cast<const float *>(stage + 2 * KT * RB);
+        float *scales = reinterpret_cast<float *>(stage + 2 * KT * RB);
+        // The value scales' logarithms in their place, a lane for each (by every lane that
+        // needs them: 32 rows of 16-32K keys of 64 columns 92 us, 94 this way; of 128
+        // 152, 149), and their signs.
+        uint32_t signs = 0;
+        if constexpr (k8) {
+            static_assert(KT == 32, "a lane for each key");
+            const float x = scales[KT + lane];
+            scales[KT + lane] = lg2_any(fabsf(x));
+            signs = __ballot_sync(kFull, signbit(x)) >> 2 * t;
+        }
         // scores
 #pragma unroll
         for (int x = 0; x < KB; ++x) {
@@ -443,6 +460,7 @@ struct MmaTile {
         }
         const uint32_t all = KT == 32 ? kFull : (1u << KT) - 1;
         uint32_t ph[NB][KB], pl[NB][KB];
+        if constexpr (k8) __syncwarp();  // the logarithms are there
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
             float top = m[b], topw = mw[b];
@@ -455,7 +473,7 @@ struct MmaTile {
                     float z = s[x][2 * b + y] * unit[b];
                     if constexpr (k8) {
                         z *= scales[key];
-                        lv[x][y] = lg2(fabsf(scales[KT + key]));
+                        lv[x][y] = scales[KT + key];
                     }
                     s[x][2 * b + y] = z;
                 }
@@ -503,9 +521,12 @@ struct MmaTile {
                 l[b] += p0 + p1;
                 if constexpr (k8) {
                     // up to 2^14, so that fp16's smallest step is 2^-38 of the largest
-                    const int key = x * 8 + 2 * t;
-                    p0 = copysignf(ex2(z0 + lv[x][0] - now + 14.f), scales[KT + key]);
-                    p1 = copysignf(ex2(z1 + lv[x][1] - now + 14.f), scales[KT + key + 1]);
+                    p0 = ex2(z0 + lv[x][0] - now + 14.f);
+                    p1 = ex2(z1 + lv[x][1] - now + 14.f);
+                    p0 = __uint_as_float(__float_as_uint(p0) ^
+                                         ((signs << (31 - 8 * x)) & 0x80000000u));
+                    p1 = __uint_as_float(__float_as_uint(p1) ^
+                                         ((signs << (30 - 8 * x)) & 0x80000000u));
                 }
                 split16(p0, p1, ph[b][x], pl[b][x], T());
             }
@@ -552,8 +573,11 @@ struct MmaTile {
         for (int b = 0; b < NB; ++b) {
             l[b] += __shfl_xor_sync(kFull, l[b], 1);
             l[b] += __shfl_xor_sync(kFull, l[b], 2);
-            // (no weight at all: the sums are zero)
-            const float back = !k8 ? 1.f : mw[b] == -INFINITY ? 0.f : ex2(mw[b] - 14.f - m[b]);
+            // The weights' unit, 2^(mw - 14 - m), by its square root, twice: value scales
+            // reach from 2^-149 to 2^128, the unit goes below 2^-126.  (No weight at all:
+            // the sums are zero.)
+            const float back =
+                !k8 ? 1.f : mw[b] == -INFINITY ? 0.f : ex2(0.5f * (mw[b] - 14.f - m[b]));
 #pragma unroll
             for (int i = 0; i < VN; ++i)
 #pragma unroll
@@ -566,7 +590,8 @@ struct MmaTile {
                             const float hi = acc[b][i * VE + e + y][c];
                             const float lo = acc[b][i * VE + e + y][2 + c];
                             // (an infinite value times a remainder of zero)
-                            o[y] = (fabsf(hi) < INFINITY ? hi + lo : hi) * back;
+                            o[y] = fabsf(hi) < INFINITY ? hi + lo : hi;
+                            if constexpr (k8) o[y] = o[y] * back * back;
                         }
                         f(b * 8 + g, (i * 8 + 2 * t + c) * VE + e,
                           make_float4(o[0], o[1], o[2], o[3]), m[b], l[b]);
