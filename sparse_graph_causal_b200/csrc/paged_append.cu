@@ -127,8 +127,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const AppendArgs
 #pragma unroll
             for (int y = 0; y < V; ++y)
                 x[w][i][y] =
-                    in ? __ldg(reinterpret_cast<const uint4 *>(a.src[w] + token[i] * a.stride[w]) +
-                               (piece[i] * V + y))
+                    in ? reinterpret_cast<const uint4 *>(a.src[w] + token[i] * a.stride[w])
+                             [piece[i] * V + y]
                        : make_uint4(0, 0, 0, 0);
     }
 #pragma unroll

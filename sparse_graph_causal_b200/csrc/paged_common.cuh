@@ -11,6 +11,8 @@
 // be launched: plan, append and decode of 64 tokens, one after the other, take
 // 10.0 us instead of 16.4 launched by themselves and 8.0 instead of 9.3 in a graph.
 // (A kernel that is not of this kind is waited for, and waits, as usual.)
+// What a kernel reads may be written while it is on the GPU already: no load of such
+// memory is a read-only one (__ldg).
 __device__ __forceinline__ void chain_begin() {
     asm volatile("griddepcontrol.launch_dependents;");
     asm volatile("griddepcontrol.wait;" ::: "memory");
