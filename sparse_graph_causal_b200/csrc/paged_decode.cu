@@ -1145,15 +1145,28 @@ int64_t longest_row(const sa_graph_s *g) {
     return n < g->T ? n : g->T;
 }
 
-// Rows that the direct way takes, by the bytes of keys and values of the longest.
-// Up to kDirectBytes it is the faster one for nearly every batch (direct and split,
+// Rows that the direct way takes, by the bytes of keys and values of the longest
+// that the graph allows (the host does not know the positions).
+//   Up to kDirectBytes it is the faster one for nearly every batch (direct and split,
 // us: 8 rows of 128 KB 5.4, 9.0; of 384 KB 9.9, 10.2; of 512 KB 12.1, 10.5; 2,048
-// rows of 128 KB 58, 56, of 384 KB 156, 139), up to kDirectSome where the rows are
-// half to four times the SMs (160 rows of 768 KB 30, 32; 512 rows 66, 77; 80 rows
-// of 512 KB 20, 21), and up to kDirectUniform where rows that nearly all have the
-// window's length fill the SMs in one go (128 rows of 2 MB: 44, 54; of 8-bit rows
-// 58, 60).
-constexpr int64_t kDirectBytes = 384 << 10, kDirectSome = 768 << 10, kDirectUniform = 2 << 20;
+// rows of 128 KB 58, 56, of 384 KB 156, 139).
+//   Up to kDirectSome where the rows are half to four times the SMs (160 bf16 rows of
+// 768 KB 31, 33, 8-bit ones 43, 37; 512 rows 66, 77; 80 rows of 512 KB 20, 21).
+//   Up to kDirectUniform on graphs of a window and up to 63 links, short of the
+// sequences, where the rows fill the SMs in one go.  A CTA needs 17 us for a MB of
+// 16-bit rows, 21 in fp32, 26 in 8 bits, the whole GPU 21 for 128 of them, and split
+// 12 more for its shares and the join.  So it depends on the positions (112 to 144
+// rows, D = 128, direct as a part of split's time):
+//     whole windows   bf16 0.75-0.79 at 1 MB, 0.83-0.88 at 2.5, 0.86-0.90 at 4;
+//                     fp32 0.76-0.79, 0.84-0.91, 0.87-0.96;  8 bits 0.84-0.87 at 1 MB,
+//                     0.87-0.93 at 1.5, 0.96-1.05 at 4
+//     from nothing to two windows, evenly   bf16 0.79-0.93, 0.88-1.06, 0.91-1.17;
+//                     fp32 0.85-0.93, 1.01-1.14, 1.07-1.23;  8 bits 0.93-1.03, 1.02-1.13
+//     one window, the others a sixteenth    bf16 1.5, 2.7, 3.7;  8 bits 1.9-2.1, 2.6
+// The limit is where batches of the second kind come out even on average, 2.5 MB, or
+// half of that in 8 bits; a batch of the third kind is slower by what one CTA takes for
+// its row (48 us at 2.5 MB, 17 in shares).
+constexpr int64_t kDirectBytes = 384 << 10, kDirectSome = 768 << 10, kDirectUniform = 2560 << 10;
 
 int64_t longest_bytes(const sa_graph_s *g, const sa_paged_cache &c) {
     return longest_row(g) * 2 * c.D * (c.dtype == SA_FP32 ? 4 : c.dtype == SA_BF16 ? 2 : 1);
@@ -1164,7 +1177,8 @@ bool is_direct(const sa_graph_s *g, const sa_paged_cache &c, int64_t rows, int s
     if (bytes <= kDirectBytes) return true;
     if (bytes <= kDirectSome && 2 * rows >= sms && rows <= 4 * sms) return true;
     const bool uniform = g->kind == 0 && g->W <= g->T / 4;
-    return bytes <= kDirectUniform && uniform && rows <= sms && 4 * rows >= 3 * sms;
+    return bytes <= (c.dtype == SA_E4M3 ? kDirectUniform / 2 : kDirectUniform) && uniform &&
+           rows <= sms && 4 * rows >= 3 * sms;
 }
 
 // f(a Tile type) for this cache and group size.
