@@ -219,8 +219,10 @@ typedef enum {
     SA_PAGED_OK = 0,
     SA_PAGED_NO_PAGES = 1, /* not enough free pages: nothing done for it */
     SA_PAGED_REFUSED = 2   /* len or n_new out of range, longer than its
-                              block-table row, past `capacity`, or its pages
-                              do not fit on the stack: nothing done for it */
+                              block-table row, past `capacity`, or, of a
+                              finished one, its pages and those of the
+                              finished ones before it do not fit on the
+                              stack: nothing done for it */
 } sa_paged_status;
 
 /* The bookkeeping of one step of a server, all arrays in DEVICE memory.
@@ -228,7 +230,10 @@ typedef enum {
  * and brings n_new[b] >= 0 new tokens, or has finished (n_new[b] = -1).  Free
  * pages lie on a stack: free_pages[0 .. *free_count).
  *   1. The pages of finished requests go on top of the stack, in the order
- *      (request, page); their length becomes 0.  Uses are not counted: a
+ *      (request, page); their length becomes 0.  Once the stack (n_stack) has
+ *      no room for all the pages of a finished request, it and every later
+ *      finished one that holds a page get SA_PAGED_REFUSED, also one whose
+ *      own pages would fit (none overtakes here either).  Uses are not counted: a
  *      page that stands in two rows (a shared prompt) would go on the stack
  *      with each of them, so of those rows only the last in use may be
  *      finished here; the owner clears the others' lengths.

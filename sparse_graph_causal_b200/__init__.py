@@ -446,7 +446,10 @@ def sparse_attn_paged_plan(length, n_new, block_table, free_pages, free_count, p
     block_table int32 [B, max_pages]; free_pages int32 [n] a stack of
     free_count (int64 [1]) pages.  block_table and free_pages are updated in
     place, and so are length and free_count unless length_out and
-    free_count_out are given.  Returns batch."""
+    free_count_out are given.  batch.status says what became of each request:
+    requests without pages, and finished ones whose pages do not fit on the
+    stack, stay as they were, and so do those like them behind (none
+    overtakes).  Returns batch."""
     if not isinstance(batch, PagedBatch):
         raise ValueError("batch must be a PagedBatch")
     status = _paged.plan(length, n_new, block_table, free_pages, free_count, page_size,
