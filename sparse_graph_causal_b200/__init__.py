@@ -127,8 +127,8 @@ class _LazyPaged:
         import importlib
         try:
             return getattr(importlib.import_module(__name__ + "._paged"), name)
-        except ModuleNotFoundError as e:
-            raise ImportError("the _paged module is not built: run "
+        except ImportError as e:  # not built, or for another torch
+            raise ImportError(f"the _paged module does not load ({e}): run "
                               "`python -m sparse_graph_causal_b200.build`") from e
 
 

@@ -4,6 +4,7 @@ marshals the paged cache's calls (host C++ on torch's headers).
 Usage: python -m sparse_graph_causal_b200.build"""
 from __future__ import annotations
 
+import importlib.metadata
 import os
 import subprocess
 import sys
@@ -29,6 +30,13 @@ def _stale(out, deps):
         return True
     t = os.path.getmtime(out)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _text(path):
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def build(verbose: bool = False, jobs: int = 8) -> str:
@@ -60,11 +68,18 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
 
 
 def build_binding(verbose: bool = False) -> str:
+    """The module holds torch's C++ interface of the version that it is built with: it is built
+    again for another one (kept beside the objects), and refuses to load next to one."""
     src = os.path.join(CSRC, "paged_py.cpp")
-    if _stale(BIND, [src, os.path.join(HERE, "..", "include", "sparse_attn.h")]):
+    stamp = os.path.join(OBJ, os.path.basename(BIND) + ".torch")
+    version = importlib.metadata.version("torch")
+    if _stale(BIND, [src, os.path.join(HERE, "..", "include", "sparse_attn.h")]) \
+            or _text(stamp) != version:
+        import torch
         from torch.utils.cpp_extension import include_paths, library_paths
         cuda = os.path.join(os.environ.get("CUDA_HOME", "/usr/local/cuda"), "include")
-        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared"]
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+               f'-DSA_TORCH_VERSION="{torch.__version__}"']
         cmd += [f"-I{p}" for p in (*include_paths(), cuda, sysconfig.get_paths()["include"])]
         cmd += [src, "-o", BIND, *(f"-L{p}" for p in library_paths()), "-lc10", "-lc10_cuda",
                 "-ltorch_cpu", "-ltorch_python", f"-L{HERE}", f"-l:{os.path.basename(LIB)}",
@@ -72,6 +87,9 @@ def build_binding(verbose: bool = False) -> str:
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
+        os.makedirs(OBJ, exist_ok=True)
+        with open(stamp, "w") as f:
+            f.write(version)
     return BIND
 
 

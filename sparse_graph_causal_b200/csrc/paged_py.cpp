@@ -209,4 +209,16 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged() { return PyModule_Create(&module); }
+// The module works on the tensors of the torch that it was built with.
+PyMODINIT_FUNC PyInit__paged() {
+    PyObject *torch = PyImport_ImportModule("torch");
+    PyObject *version = torch ? PyObject_GetAttrString(torch, "__version__") : nullptr;
+    const char *v = version ? PyUnicode_AsUTF8(version) : nullptr;
+    const bool same = v && std::string(v) == SA_TORCH_VERSION;
+    if (v && !same)
+        PyErr_Format(PyExc_ImportError,
+                     "built for torch %s, torch is %s", SA_TORCH_VERSION, v);
+    Py_XDECREF(version);
+    Py_XDECREF(torch);
+    return same ? PyModule_Create(&module) : nullptr;
+}
