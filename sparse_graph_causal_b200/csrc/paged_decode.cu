@@ -6,9 +6,9 @@
 // query heads of its group together, so the work is HBM traffic: 2 D es bytes
 // for 4 G D operations, G query heads to a cache head.  Everything below is
 // there to keep the loads in flight.  16 rows of 4,096 keys (8 cache heads of 128
-// columns, bf16) take 45 us, 5.9 TB/s; one of 131,072 keys 93 us, 5.8 TB/s; 48
+// columns, bf16) take 46 us, 5.8 TB/s; one of 131,072 keys 95 us, 5.7 TB/s; 48
 // ragged ones in 8 bits (101 MB) 30 us, of which 8 are the start of the shares
-// and the join.
+// and the join (new inputs from call to call).
 //
 // A warp owns a run of one row's edges and gathers them tile by tile with
 // cp.async: rows are addressed one by one (edge -> position -> page -> cache
@@ -30,7 +30,10 @@
 //   8-bit rows become fp16 exactly.  A query row is scaled by a power of two
 // into fp16's range; a value row's scale goes into its weight, and the weights
 // have a running maximum of their own, so that no choice of scales overflows or
-// loses them.
+// loses them.  It goes in by its logarithm, weight = 2^(score + log2 scale - max):
+// one exponential instead of a product whose range fp16 lacks, at the price of the
+// logarithm's 2^-22 of its size (2^-19 of the weight for scales around 2^-10, 2^-15 at
+// 2^-149), which the output's rounding by 2^-8 covers.
 //
 // fp32 caches: CUDA cores, a lane per key for the scores, a lane per four
 // columns for the values, both from the staged tile.

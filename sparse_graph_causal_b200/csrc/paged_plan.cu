@@ -14,8 +14,9 @@
 //
 // Nothing here is worth a byte of bandwidth (20 bytes a token, 40 a request):
 // the step is bound by its chain of dependent loads, barriers and launches, so
-// it is one launch, a single CTA or one cluster (64 requests of one token 3.2 us;
-// 2,000 requests with 60,000 tokens 11.3 us, 15.6 with eight CTAs).  Every CTA runs the scans of
+// it is one launch, a single CTA or one cluster (64 requests of one token 3.3 us a
+// call in a graph, 3.7 on a stream; 2,000 requests with 60,000 tokens 11.3 and 11.5,
+// with eight CTAs 15.6).  Every CTA runs the scans of
 // all requests by itself and keeps what the tokens need in its shared memory;
 // then the CTAs share the tokens, each found by bisection.  A cluster barrier
 // orders every read of the lengths before the writes of the new ones (which
