@@ -18,7 +18,7 @@ CHAINED = sorted(f for f in os.listdir(CSRC) if f.endswith(".cu") and "launch_ch
 
 
 def test_there_are_chained_kernels():
-    assert CHAINED == ["paged_append.cu", "paged_decode.cu", "paged_plan.cu"]
+    assert {"paged_append.cu", "paged_decode.cu", "paged_plan.cu"} <= set(CHAINED)
 
 
 @pytest.mark.parametrize("name", CHAINED)
